@@ -206,6 +206,8 @@ def _own_diff(s):
     case = s["case"]
     flags = sva.SVA_FLAG_LAMBDA_VALUE if case["lam"] == "head" else 0
     more = dict(key_lens=s["key_lens"], flags=flags)
+    if case["train"] and s["saved"][0].dtype != torch.float32:  # the two maps' outputs are kept in 32 bits
+        s["saved"] = (*(torch.empty_like(o, dtype=torch.float32) for o in s["saved"][:2]), s["saved"][2])
     s["ws"] = sva.sva_diff_anchor_fwd(s["q"], s["k"], s["v"], s["gate"], s["lam"], s["out"], case["H"],
                                       saved=s.get("saved"), ws=s["ws"], **more)
     if not case["train"]:
