@@ -65,6 +65,10 @@ typedef enum { SVA_F32 = 0, SVA_BF16 = 1 } sva_dtype_t;
  * (linear attention only; lets a producer that applied the feature map skip it). */
 #define SVA_FLAG_QK_FEATURES 1u
 
+/* sva_diff_args.flags: lam holds the weight lambda of the second map itself, not
+ * the logit of a sigmoid. */
+#define SVA_FLAG_LAMBDA_VALUE 2u
+
 /* Arguments of one attention-core call over all B*H (batch, head) pairs. */
 typedef struct {
   int B, N, H, d;        /* batch, tokens, heads, head dim; D = H*d           */
@@ -162,6 +166,141 @@ sva_status_t sva_linear_attn_fwd_noalloc(const sva_attn_args* args, sva_stream_t
 size_t sva_softmax_anchor_workspace_bytes(int B, int N, int H, int d, sva_dtype_t dtype);
 sva_status_t sva_softmax_anchor_fwd(const sva_attn_args* args, void* ws, size_t ws_bytes,
                                     sva_stream_t stream);
+
+/*
+ * Gated differential softmax anchor (non-causal): the anchor with a second
+ * softmax map subtracted from the first, which cancels the attention that both
+ * maps spend on the same unrelated tokens. A drop-in for the anchor in width:
+ * the d query and key columns of a head are two maps of d/2 each (map 1 owns
+ * columns [h*d, h*d + d/2), map 2 the rest), the value head is whole, so the
+ * fused projection keeps its 4D columns. Per batch b and head h:
+ *     P_m[t, s] = softmax_s(scale * Q_m[t] . K_m[s]) over s < key_lens[b], m = 1, 2
+ *     A_t   = sum_s (P_1[t, s] - lambda_t P_2[t, s]) V_s
+ *     out_t = A_t * sigmoid(G_t)          (out_t = A_t without a gate)
+ * lambda_t = sigmoid(lam[b, t, h]) with lam's row stride ldl >= H, or with ldl
+ * = 0 the same lam[h] for every token; with SVA_FLAG_LAMBDA_VALUE lambda is lam
+ * itself. lam is in dtype (per-token logits can come out of the same projection
+ * as Q, K, V and G).
+ * Keys at or behind key_lens[b] count for nothing, whatever their rows of k and
+ * v hold (NaN and infinities too); a value outside [0, n_keys] is taken as the
+ * nearer end. A batch with no key gives A = 0. All N query rows are computed.
+ * Supported: SVA_BF16 with d = 128 (tcgen05 kernels), SVA_F32 with d in
+ * {64, 128}. Any N >= 1 and n_keys >= 1.
+ *
+ * Training: give o1, o2 (fp32 [B, N, D], contiguous: the two maps' outputs
+ * P_m V; in 32 bits, since dG and dlambda are made of them) and lse (fp32
+ * [2][B][H][N]: log-sum-exp of each map's scaled logits, -infinity where a batch has no key) to the forward call, all three or none,
+ * and the same to sva_diff_anchor_bwd, which computes from dout ([B, N, >=D])
+ *     dA = dout * sigmoid(G),  dG = dout * A * sigmoid'(G)
+ *     delta_m[t] = dA_t . O_m[t],  dlambda_t = -delta_2[t]
+ *     dV = (P_1 - lambda P_2)^T dA,   dP = dA V^T
+ *     dS_1 = P_1 (dP - delta_1),   dS_2 = -lambda P_2 (dP - delta_2)
+ *     dQ_m = scale dS_m K_m,   dK_m = scale dS_m^T Q_m
+ * dq, dk, dv, dgate are laid out as q, k, v, gate (row strides of their own);
+ * dlam as lam: [B, N, >=H] with row stride lddl, or with ldl = 0 the sum over
+ * all tokens, [H]; each in dtype. dgate must be NULL exactly when gate is. All
+ * gradients are written whole (not added to), dk and dv with zeros at and
+ * behind key_lens[b]. A padded batch's own padding among the queries takes part
+ * unless its dout rows are zero (and its q rows finite). Gradients may not
+ * overlap the inputs. No atomics: the same call gives the same bits.
+ */
+typedef struct {
+  int B, N, H, d;        /* batch, query tokens, heads, head dim; D = H*d      */
+  int n_keys;            /* rows of k and v; 0 means N                         */
+  sva_dtype_t dtype;
+  const void* q;    int64_t ldq;   /* [B, N, >=D]                              */
+  const void* k;    int64_t ldk;   /* [B, n_keys, >=D]                         */
+  const void* v;    int64_t ldv;   /* [B, n_keys, >=D]                         */
+  const void* gate; int64_t ldg;   /* nullable [B, N, >=D] gate logits         */
+  const void* lam;  int64_t ldl;   /* [B, N, >=H], or ldl = 0: [H]             */
+  const int32_t* key_lens;         /* nullable, device, [B]                    */
+  void* out;        int64_t ldo;   /* [B, N, >=D] (forward)                    */
+  float scale;           /* logit scale; 0 means 1/sqrt(d/2)                   */
+  unsigned flags;        /* SVA_FLAG_LAMBDA_VALUE                              */
+  float* o1;             /* saved for the backward pass; nullable (forward)    */
+  float* o2;
+  float* lse;
+} sva_diff_args;
+
+typedef struct {
+  const void* dout; int64_t lddo;  /* [B, N, >=D]                              */
+  void* dq;    int64_t lddq;
+  void* dk;    int64_t lddk;
+  void* dv;    int64_t lddv;
+  void* dgate; int64_t lddg;       /* NULL without a gate                      */
+  void* dlam;  int64_t lddl;       /* row stride as ldl's rule; 0 iff ldl is 0 */
+} sva_diff_grads;
+
+size_t sva_diff_anchor_workspace_bytes(int B, int N, int H, int d, int n_keys, sva_dtype_t dtype);
+sva_status_t sva_diff_anchor_fwd(const sva_diff_args* args, void* ws, size_t ws_bytes,
+                                 sva_stream_t stream);
+size_t sva_diff_anchor_bwd_workspace_bytes(int B, int N, int H, int d, int n_keys,
+                                           sva_dtype_t dtype);
+sva_status_t sva_diff_anchor_bwd(const sva_diff_args* args, const sva_diff_grads* grads, void* ws,
+                                 size_t ws_bytes, sva_stream_t stream);
+
+/*
+ * The norms around a block, fused with the block's gate and the residual
+ * update. Between two layers of a stack this is one call: the norm behind the
+ * block that just ran, its gate, the residual scale and the residual update of
+ * the fp32 stream, then the norm before the next block with its modulation.
+ * Per token t of batch b, over the D channels:
+ *     h'_t = res_scale * h_t + gate_b * (Norm(o_t) * w_post)       (with o)
+ *     h'_t = h_t                                                   (without o)
+ *     u_t  = Norm(h'_t) * w_pre * (1 + scale_b) + shift_b          (with u)
+ *     Norm(x) = x / sqrt(mean(x^2) + eps)                          (SVA_NORM_RMS)
+ *     Norm(x) = (x - mean x) / sqrt(mean((x - mean x)^2) + eps)    (SVA_NORM_LAYER)
+ * o and u may each be NULL, not both; h_out (h') is required with o and not
+ * used without it; it may alias h. w_post, w_pre ([D]), gate, scale, shift
+ * ([B, >=D], one row per batch) are in dtype and nullable (1, 1, 1, 0, 0).
+ * Modulation per frame: pass B * frames as B. h and h' are fp32. Statistics
+ * and sums are fp32. 1 <= D <= 8192; B * N < 2^31.
+ *
+ * Training: give stats (fp32 [B*N][4], 16-byte aligned) to the forward call and
+ * to sva_block_norm_bwd, which takes dh_out (the gradient of h', fp32, nullable
+ * = 0) and du (the gradient of u, required with u) and writes dh (fp32, may
+ * alias dh_out), d_o (dtype, with o; may alias o) and, each nullable, the sums
+ * over tokens dw_post, dw_pre ([D]) and dgate, dscale, dshift ([B, D]), all
+ * fp32 and contiguous. In args it reads h_out (h without o), o, stats, the
+ * weights and modulation, and u only for being NULL or not. No atomics.
+ */
+typedef enum { SVA_NORM_RMS = 0, SVA_NORM_LAYER = 1 } sva_norm_kind_t;
+
+typedef struct {
+  int B, N, D;
+  sva_dtype_t dtype;
+  sva_norm_kind_t kind;
+  float eps;
+  float res_scale;
+  const float* h;      int64_t ldh;      /* [B, N, >=D] fp32 residual stream      */
+  const void* o;       int64_t ldo;      /* nullable [B, N, >=D]: block's output  */
+  const void* w_post;                    /* nullable [D]                          */
+  const void* gate;    int64_t ldgate;   /* nullable [B, >=D]                     */
+  float* h_out;        int64_t ldho;     /* [B, N, >=D] fp32, with o              */
+  const void* w_pre;                     /* nullable [D]                          */
+  const void* scale;   int64_t ldscale;  /* nullable [B, >=D]                     */
+  const void* shift;   int64_t ldshift;  /* nullable [B, >=D]                     */
+  void* u;             int64_t ldu;      /* nullable [B, N, >=D]                  */
+  float* stats;                          /* nullable in the forward pass          */
+} sva_block_norm_args;
+
+typedef struct {
+  const float* dh_out; int64_t lddho;    /* nullable [B, N, >=D] fp32             */
+  const void* du;      int64_t lddu;     /* [B, N, >=D], with u                   */
+  float* dh;           int64_t lddh;     /* [B, N, >=D] fp32                      */
+  void* d_o;           int64_t lddo;     /* [B, N, >=D], with o                   */
+  float* dw_post;                        /* nullable [D]                          */
+  float* dgate;                          /* nullable [B, D]                       */
+  float* dw_pre;                         /* nullable [D]                          */
+  float* dscale;                         /* nullable [B, D]                       */
+  float* dshift;                         /* nullable [B, D]                       */
+} sva_block_norm_grads;
+
+sva_status_t sva_block_norm_fwd(const sva_block_norm_args* args, sva_stream_t stream);
+size_t sva_block_norm_bwd_workspace_bytes(int B, int N, int D);
+sva_status_t sva_block_norm_bwd(const sva_block_norm_args* args,
+                                const sva_block_norm_grads* grads, void* ws, size_t ws_bytes,
+                                sva_stream_t stream);
 
 /*
  * Projections of a mixer layer: y = x W^T with x [M, K] (row stride ldx),

@@ -22,6 +22,8 @@ SVA_ERR_WORKSPACE, SVA_ERR_CUDA, SVA_ERR_DEVICE_TIMEOUT = 3, 4, 5
 SVA_F32, SVA_BF16 = 0, 1
 SVA_STATUS_BYTES = 256
 SVA_FLAG_QK_FEATURES = 1
+SVA_FLAG_LAMBDA_VALUE = 2
+SVA_NORM_RMS, SVA_NORM_LAYER = 0, 1
 KERNEL_CLASSES = ("proj_qkvg", "proj_out", "linear_state", "linear_readout", "anchor", "route",
                   "keys", "other", "linear_reduce")
 
@@ -50,6 +52,61 @@ class AttnArgs(ctypes.Structure):
         ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("flags", ctypes.c_uint),
         ("wgate", ctypes.c_void_p), ("ldw", ctypes.c_int64),
         ("n_keys", ctypes.c_int),
+    ]
+
+
+class DiffArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+        ("n_keys", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("ldk", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64),
+        ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+        ("lam", ctypes.c_void_p), ("ldl", ctypes.c_int64),
+        ("key_lens", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+        ("scale", ctypes.c_float), ("flags", ctypes.c_uint),
+        ("o1", ctypes.c_void_p), ("o2", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
+class DiffGrads(ctypes.Structure):
+    _fields_ = [
+        ("dout", ctypes.c_void_p), ("lddo", ctypes.c_int64),
+        ("dq", ctypes.c_void_p), ("lddq", ctypes.c_int64),
+        ("dk", ctypes.c_void_p), ("lddk", ctypes.c_int64),
+        ("dv", ctypes.c_void_p), ("lddv", ctypes.c_int64),
+        ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64),
+        ("dlam", ctypes.c_void_p), ("lddl", ctypes.c_int64),
+    ]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("kind", ctypes.c_int), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+        ("w_post", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("ldgate", ctypes.c_int64),
+        ("h_out", ctypes.c_void_p), ("ldho", ctypes.c_int64),
+        ("w_pre", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p), ("ldscale", ctypes.c_int64),
+        ("shift", ctypes.c_void_p), ("ldshift", ctypes.c_int64),
+        ("u", ctypes.c_void_p), ("ldu", ctypes.c_int64),
+        ("stats", ctypes.c_void_p),
+    ]
+
+
+class BlockNormGrads(ctypes.Structure):
+    _fields_ = [
+        ("dh_out", ctypes.c_void_p), ("lddho", ctypes.c_int64),
+        ("du", ctypes.c_void_p), ("lddu", ctypes.c_int64),
+        ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+        ("d_o", ctypes.c_void_p), ("lddo", ctypes.c_int64),
+        ("dw_post", ctypes.c_void_p), ("dgate", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p),
+        ("dscale", ctypes.c_void_p), ("dshift", ctypes.c_void_p),
     ]
 
 
@@ -86,6 +143,17 @@ _SIGS = {
     "sva_softmax_anchor_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 5),
     "sva_softmax_anchor_fwd": (ctypes.c_int, [ctypes.POINTER(AttnArgs), ctypes.c_void_p,
                                               ctypes.c_size_t, ctypes.c_void_p]),
+    "sva_diff_anchor_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "sva_diff_anchor_fwd": (ctypes.c_int, [ctypes.POINTER(DiffArgs), ctypes.c_void_p,
+                                           ctypes.c_size_t, ctypes.c_void_p]),
+    "sva_diff_anchor_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "sva_diff_anchor_bwd": (ctypes.c_int, [ctypes.POINTER(DiffArgs), ctypes.POINTER(DiffGrads),
+                                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "sva_block_norm_fwd": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), ctypes.c_void_p]),
+    "sva_block_norm_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 3),
+    "sva_block_norm_bwd": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs),
+                                          ctypes.POINTER(BlockNormGrads), ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p]),
     "sva_projection_workspace_bytes": (ctypes.c_size_t, []),
     "sva_projection_fwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                           ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
@@ -313,6 +381,221 @@ def sva_softmax_anchor_fwd(q, k, v, gate, out, H: int, residual=None, scale: flo
     ws = workspace(need, q.device) if ws is None else ws
     _check(_lib().sva_softmax_anchor_fwd(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)),
            "sva_softmax_anchor_fwd")
+    return ws
+
+
+def _same_dtype(dt, **tensors):
+    for name, t in tensors.items():
+        if t is not None and _dtype_code(t) != dt:
+            raise TypeError(f"{name} must have the dtype of the call's activations")
+
+
+def _width(t, W: int, name: str):
+    if t.shape[-1] < W:
+        raise ValueError(f"{name} must be at least {W} wide, got {tuple(t.shape)}")
+
+
+def _lam_stride(lam, B: int, N: int, H: int, name: str) -> int:
+    """Row stride of per-token lambdas [B, N, >=H]; 0 for the shared form [H]."""
+    if not lam.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if lam.dim() == 1:
+        if lam.shape[0] != H or lam.stride(0) != 1:
+            raise ValueError(f"expected {name} [H={H}] contiguous, got {tuple(lam.shape)}")
+        return 0
+    ld = _rows(lam, B, N)
+    _width(lam, H, name)
+    return ld
+
+
+def _diff_args(q, k, v, gate, lam, out, H, key_lens, scale, flags, saved) -> DiffArgs:
+    torch = _torch()
+    B, N, D = q.shape
+    Nk = k.shape[1]
+    if D % H:
+        raise ValueError(f"width {D} is not a multiple of H={H}")
+    dt = _dtype_code(q)
+    _same_dtype(dt, k=k, v=v, gate=gate, lam=lam, out=out)
+    a = DiffArgs()
+    a.B, a.N, a.H, a.d, a.dtype = B, N, H, D // H, dt
+    a.n_keys = Nk if Nk != N else 0
+    a.q, a.ldq = _ptr(q), _rows(q, B, N)
+    a.k, a.ldk = _ptr(k), _rows(k, B, Nk)
+    a.v, a.ldv = _ptr(v), _rows(v, B, Nk)
+    for name, t in (("k", k), ("v", v), ("gate", gate), ("out", out)):
+        if t is not None:
+            _width(t, D, name)
+    if gate is not None:
+        a.gate, a.ldg = _ptr(gate), _rows(gate, B, N)
+    a.lam, a.ldl = _ptr(lam), _lam_stride(lam, B, N, H, "lam")
+    if key_lens is not None:
+        if key_lens.dtype != torch.int32 or key_lens.shape != (B,) or not key_lens.is_contiguous() \
+                or not key_lens.is_cuda:
+            raise ValueError(f"key_lens must be a contiguous int32 CUDA tensor of {B} values")
+        a.key_lens = _ptr(key_lens)
+    if out is not None:
+        a.out, a.ldo = _ptr(out), _rows(out, B, N)
+    a.scale, a.flags = float(scale), int(flags)
+    if saved is not None:
+        o1, o2, lse = saved
+        for t, shape in ((o1, (B, N, D)), (o2, (B, N, D)), (lse, (2, B, H, N))):
+            if tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError("saved must be contiguous CUDA tensors o1, o2 [B, N, D] and "
+                                 f"lse [2, B, H, N], got {tuple(t.shape)}")
+            if t.dtype != torch.float32:
+                raise TypeError("saved tensors must be float32")
+        a.o1, a.o2, a.lse = _ptr(o1), _ptr(o2), _ptr(lse)
+    return a
+
+
+def sva_diff_anchor_workspace_bytes(B: int, N: int, H: int, d: int, n_keys: int, dtype: int) -> int:
+    return int(_lib().sva_diff_anchor_workspace_bytes(B, N, H, d, n_keys, dtype))
+
+
+def sva_diff_anchor_fwd(q, k, v, gate, lam, out, H: int, key_lens=None, scale: float = 0.0,
+                        flags: int = 0, saved=None, ws=None, stream=None):
+    """Gated differential anchor: out = (P_1 V - lambda P_2 V) * sigmoid(G), the two maps'
+    queries and keys being the halves of each head's columns. gate may be None. lam: logits
+    [B, N, >=H] or [H] (lambda itself with SVA_FLAG_LAMBDA_VALUE). key_lens [B] int32: keys
+    of each batch. saved (o1, o2, lse): written for sva_diff_anchor_bwd."""
+    a = _diff_args(q, k, v, gate, lam, out, H, key_lens, scale, flags, saved)
+    if ws is None:
+        ws = workspace(sva_diff_anchor_workspace_bytes(a.B, a.N, a.H, a.d, a.n_keys, a.dtype),
+                       q.device)
+    _check(_lib().sva_diff_anchor_fwd(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)),
+           "sva_diff_anchor_fwd")
+    return ws
+
+
+def sva_diff_anchor_bwd_workspace_bytes(B: int, N: int, H: int, d: int, n_keys: int,
+                                        dtype: int) -> int:
+    return int(_lib().sva_diff_anchor_bwd_workspace_bytes(B, N, H, d, n_keys, dtype))
+
+
+def sva_diff_anchor_bwd(q, k, v, gate, lam, dout, saved, dq, dk, dv, dgate, dlam, H: int,
+                        key_lens=None, scale: float = 0.0, flags: int = 0, ws=None, stream=None):
+    """Gradients of sva_diff_anchor_fwd for the same arguments and its saved tensors; dgate is
+    None exactly when gate is; dlam is laid out as lam."""
+    if saved is None:
+        raise ValueError("the backward pass needs the forward pass's saved (o1, o2, lse)")
+    a = _diff_args(q, k, v, gate, lam, None, H, key_lens, scale, flags, saved)
+    D, Nk = a.H * a.d, k.shape[1]
+    _same_dtype(a.dtype, dout=dout, dq=dq, dk=dk, dv=dv, dgate=dgate, dlam=dlam)
+    g = DiffGrads()
+    for name, t, n in (("dout", dout, a.N), ("dq", dq, a.N), ("dk", dk, Nk), ("dv", dv, Nk),
+                       ("dgate", dgate, a.N)):
+        if t is not None:
+            _width(t, D, name)
+            setattr(g, name, _ptr(t))
+            setattr(g, {"dout": "lddo", "dgate": "lddg"}.get(name, "ld" + name), _rows(t, a.B, n))
+    g.dlam, g.lddl = _ptr(dlam), _lam_stride(dlam, a.B, a.N, a.H, "dlam")
+    if ws is None:
+        ws = workspace(sva_diff_anchor_bwd_workspace_bytes(a.B, a.N, a.H, a.d, a.n_keys, a.dtype),
+                       q.device)
+    _check(_lib().sva_diff_anchor_bwd(ctypes.byref(a), ctypes.byref(g), _ptr(ws), ws.numel(),
+                                      _stream(stream)), "sva_diff_anchor_bwd")
+    return ws
+
+
+def _batch_rows(t, B: int, D: int, name: str):
+    """Row stride of a per-batch modulation [B, >=D]."""
+    if t.dim() != 2 or t.shape[0] != B or t.stride(1) != 1 or not t.is_cuda:
+        raise ValueError(f"expected a CUDA tensor {name} [B={B}, >={D}] of unit-stride rows, "
+                         f"got {tuple(t.shape)}")
+    _width(t, D, name)
+    return t.stride(0) if B > 1 else max(t.stride(0), D)
+
+
+def _norm_args(h, o, w_post, gate, h_out, w_pre, scale, shift, u, kind, eps, res_scale,
+               stats, dtype_of) -> BlockNormArgs:
+    torch = _torch()
+    B, N, D = h.shape
+    a = BlockNormArgs()
+    a.B, a.N, a.D, a.dtype = B, N, D, _dtype_code(dtype_of)
+    a.kind, a.eps, a.res_scale = int(kind), float(eps), float(res_scale)
+    _same_dtype(a.dtype, o=o, w_post=w_post, gate=gate, w_pre=w_pre, scale=scale, shift=shift, u=u)
+    for name, t, ld in (("h", h, "ldh"), ("h_out", h_out, "ldho"), ("o", o, "ldo"), ("u", u, "ldu")):
+        if t is None:
+            continue
+        if name in ("h", "h_out") and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32")
+        _width(t, D, name)
+        setattr(a, name, _ptr(t))
+        setattr(a, ld, _rows(t, B, N))
+    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+        if t is not None:
+            if tuple(t.shape) != (D,) or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"expected a contiguous CUDA tensor {name} [D={D}]")
+            setattr(a, name, _ptr(t))
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            setattr(a, name, _ptr(t))
+            setattr(a, "ld" + name, _batch_rows(t, B, D, name))
+    if stats is not None:
+        if stats.dtype != torch.float32 or not stats.is_contiguous() or not stats.is_cuda \
+                or stats.numel() < 4 * B * N:
+            raise ValueError("stats must be a contiguous float32 CUDA tensor of 4 values per token")
+        a.stats = _ptr(stats)
+    return a
+
+
+def sva_block_norm_fwd(h, o=None, w_post=None, gate=None, h_out=None, w_pre=None, scale=None,
+                       shift=None, u=None, kind: int = SVA_NORM_RMS, eps: float = 1e-6,
+                       res_scale: float = 1.0, stats=None, stream=None):
+    """h_out = res_scale h + gate * (Norm(o) * w_post) (with o), then u = Norm(h_out) * w_pre *
+    (1 + scale) + shift (with u). h, h_out fp32 [B, N, D]; o, u [B, N, D]; weights [D];
+    gate, scale, shift one row per batch [B, D]; stats [B, N, 4] fp32: written for
+    sva_block_norm_bwd."""
+    dtype_of = o if o is not None else u
+    if dtype_of is None:
+        raise ValueError("one of o and u is needed")
+    a = _norm_args(h, o, w_post, gate, h_out, w_pre, scale, shift, u, kind, eps, res_scale, stats,
+                   dtype_of)
+    _check(_lib().sva_block_norm_fwd(ctypes.byref(a), _stream(stream)), "sva_block_norm_fwd")
+
+
+def sva_block_norm_bwd_workspace_bytes(B: int, N: int, D: int) -> int:
+    return int(_lib().sva_block_norm_bwd_workspace_bytes(B, N, D))
+
+
+def sva_block_norm_bwd(h_out, stats, dh, dh_out=None, o=None, do=None, du=None, w_post=None,
+                       gate=None, w_pre=None, scale=None, dw_post=None, dgate=None, dw_pre=None,
+                       dscale=None, dshift=None, kind: int = SVA_NORM_RMS, eps: float = 1e-6,
+                       res_scale: float = 1.0, ws=None, stream=None):
+    """Gradients of sva_block_norm_fwd. h_out: its result (h in a call without o); stats: as it
+    wrote them; dh_out, du: the gradients of h_out and u. Writes dh, do and the sums over
+    tokens dw_post, dw_pre [D] and dgate, dscale, dshift [B, D] (fp32) that are given."""
+    torch = _torch()
+    dtype_of = o if o is not None else du
+    if dtype_of is None:
+        raise ValueError("one of o and du is needed")
+    # u takes part only by being there: du stands in its place
+    a = _norm_args(h_out, o, w_post, gate, h_out if o is not None else None, w_pre, scale, None, du,
+                   kind, eps, res_scale, stats, dtype_of)
+    B, N, D = h_out.shape
+    g = BlockNormGrads()
+    _same_dtype(a.dtype, do=do, du=du)
+    for name, t, ld in (("dh_out", dh_out, "lddho"), ("du", du, "lddu"), ("dh", dh, "lddh"),
+                        ("d_o", do, "lddo")):
+        if t is None:
+            continue
+        if name in ("dh_out", "dh") and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32")
+        _width(t, D, name)
+        setattr(g, name, _ptr(t))
+        setattr(g, ld, _rows(t, B, N))
+    for name, t, shape in (("dw_post", dw_post, (D,)), ("dgate", dgate, (B, D)),
+                           ("dw_pre", dw_pre, (D,)), ("dscale", dscale, (B, D)),
+                           ("dshift", dshift, (B, D))):
+        if t is not None:
+            if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() \
+                    or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous float32 CUDA tensor {shape}")
+            setattr(g, name, _ptr(t))
+    if ws is None:
+        ws = workspace(sva_block_norm_bwd_workspace_bytes(B, N, D), h_out.device)
+    _check(_lib().sva_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), _ptr(ws), ws.numel(),
+                                     _stream(stream)), "sva_block_norm_bwd")
     return ws
 
 

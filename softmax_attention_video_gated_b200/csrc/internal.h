@@ -118,6 +118,33 @@ cudaError_t anchor_bf16(const sva_attn_args& a, int* status, void* scratch, cuda
                         Prof* prof = nullptr);
 cudaError_t anchor_f32(const sva_attn_args& a, int* status, cudaStream_t s);
 
+// ---------------------------------------------------------------- differential anchor
+// Key split of a forward call: the keys of every (batch, head, query tile) are
+// cut into `split` runs of key blocks; with split > 1 each part leaves its two
+// maps' unnormalised outputs, running maxima and sums in scratch and a merge
+// kernel joins them.
+struct DiffPlan {
+  int rows = 0, keys = 0;        // tile: query rows, keys of one block
+  int n_qtiles = 0, n_kblocks = 0, split = 1;
+  size_t partial_bytes = 0;
+};
+DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt);
+cudaError_t diff_fwd_f32(const sva_diff_args& a, int* status, void* scratch, cudaStream_t s);
+// Scratch of a backward call: dA (dtype, [B*N, D]), then the queries' statistics
+// (per batch, head and 64-query tile) and dlambda per token (fp32).
+struct DiffBwdPlan {
+  size_t stats_off = 0, dlam_off = 0, total = 0;
+};
+DiffBwdPlan diff_bwd_plan(int B, int N, int H, int d, sva_dtype_t dt);
+cudaError_t diff_bwd_f32(const sva_diff_args& a, const sva_diff_grads& g, int* status,
+                         void* scratch, cudaStream_t s);
+
+// ---------------------------------------------------------------- block norms
+size_t block_norm_partial_bytes(int B, int N, int D);
+cudaError_t block_norm_fwd(const sva_block_norm_args& a, cudaStream_t s);
+cudaError_t block_norm_bwd(const sva_block_norm_args& a, const sva_block_norm_grads& g,
+                           void* scratch, cudaStream_t s);
+
 // ---------------------------------------------------------------- router
 cudaError_t route(const float* h, const void* const* keys, const void* const* summaries,
                   int n_blocks, void* u, float* alpha, int64_t rows, int D, sva_dtype_t dt,

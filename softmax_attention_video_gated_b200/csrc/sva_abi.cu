@@ -237,6 +237,202 @@ extern "C" sva_status_t sva_softmax_anchor_fwd(const sva_attn_args* args, void* 
 }
 
 // ---------------------------------------------------------------------------
+// differential anchor
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// everything but out (forward) and the saved tensors, which the two directions use differently
+sva_status_t check_diff(const sva_diff_args* a) {
+  if (a == nullptr) return SVA_ERR_INVALID_ARGUMENT;
+  if (a->dtype != SVA_F32 && a->dtype != SVA_BF16) return SVA_ERR_INVALID_ARGUMENT;
+  if (a->B < 1 || a->N < 1 || a->H < 1 || a->d < 1 || a->n_keys < 0)
+    return SVA_ERR_INVALID_ARGUMENT;
+  const int64_t D = static_cast<int64_t>(a->H) * a->d;
+  const void* ptrs[4] = {a->q, a->k, a->v, a->gate};
+  const int64_t lds[4] = {a->ldq, a->ldk, a->ldv, a->ldg};
+  for (int i = 0; i < 4; ++i) {
+    if (i == 3 && a->gate == nullptr) break;
+    if (ptrs[i] == nullptr || !aligned16(ptrs[i]) || !ld_ok(lds[i], D, a->dtype))
+      return SVA_ERR_INVALID_ARGUMENT;
+  }
+  if (a->lam == nullptr || reinterpret_cast<uintptr_t>(a->lam) % esize(a->dtype) != 0 ||
+      (a->ldl != 0 && a->ldl < a->H))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (reinterpret_cast<uintptr_t>(a->key_lens) % 4 != 0) return SVA_ERR_INVALID_ARGUMENT;
+  if (!(std::isfinite(a->scale) && a->scale >= 0.f)) return SVA_ERR_INVALID_ARGUMENT;
+  if ((a->flags & ~SVA_FLAG_LAMBDA_VALUE) != 0) return SVA_ERR_INVALID_ARGUMENT;
+  const bool any = a->o1 != nullptr || a->o2 != nullptr || a->lse != nullptr;
+  const bool all = a->o1 != nullptr && a->o2 != nullptr && a->lse != nullptr;
+  if (any && (!all || !aligned16(a->o1) || !aligned16(a->o2) ||
+              (reinterpret_cast<uintptr_t>(a->lse) & 3)))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (static_cast<int64_t>(a->B) * std::max(a->N, a->n_keys) > INT32_MAX ||
+      static_cast<int64_t>(a->B) * a->H > 65535)
+    return SVA_ERR_UNSUPPORTED;
+  if (a->dtype == SVA_BF16 && a->d != 128) return SVA_ERR_UNSUPPORTED;
+  if (a->dtype == SVA_F32 && a->d != 64 && a->d != 128) return SVA_ERR_UNSUPPORTED;
+  return SVA_OK;
+}
+
+bool diff_sizes_ok(int B, int N, int H, int d, int n_keys) {
+  return B >= 1 && N >= 1 && H >= 1 && d >= 1 && n_keys >= 0;
+}
+
+}  // namespace
+
+extern "C" size_t sva_diff_anchor_workspace_bytes(int B, int N, int H, int d, int n_keys,
+                                                  sva_dtype_t dtype) {
+  if (!diff_sizes_ok(B, N, H, d, n_keys)) return 0;
+  return SVA_STATUS_BYTES + diff_plan(B, N, H, d, n_keys, dtype).partial_bytes;
+}
+
+extern "C" sva_status_t sva_diff_anchor_fwd(const sva_diff_args* args, void* ws, size_t ws_bytes,
+                                            sva_stream_t stream) {
+  sva_status_t st = check_diff(args);
+  if (args != nullptr && st == SVA_OK &&
+      (args->out == nullptr || !aligned16(args->out) ||
+       !ld_ok(args->ldo, static_cast<int64_t>(args->H) * args->d, args->dtype)))
+    st = SVA_ERR_INVALID_ARGUMENT;
+  if (st != SVA_OK) return st;
+  if (ws == nullptr || !aligned16(ws) ||
+      ws_bytes < sva_diff_anchor_workspace_bytes(args->B, args->N, args->H, args->d, args->n_keys,
+                                                 args->dtype))
+    return SVA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = clear_status(ws, s)) != SVA_OK) return st;
+  void* scratch = static_cast<char*>(ws) + SVA_STATUS_BYTES;
+  const cudaError_t e = diff_fwd_f32(*args, static_cast<int*>(ws), scratch, s);
+  return e == cudaSuccess ? SVA_OK : cuda_fail(e);
+}
+
+extern "C" size_t sva_diff_anchor_bwd_workspace_bytes(int B, int N, int H, int d, int n_keys,
+                                                      sva_dtype_t dtype) {
+  if (!diff_sizes_ok(B, N, H, d, n_keys)) return 0;
+  return SVA_STATUS_BYTES + diff_bwd_plan(B, N, H, d, dtype).total;
+}
+
+extern "C" sva_status_t sva_diff_anchor_bwd(const sva_diff_args* args, const sva_diff_grads* grads,
+                                            void* ws, size_t ws_bytes, sva_stream_t stream) {
+  sva_status_t st = check_diff(args);
+  if (st != SVA_OK) return st;
+  if (grads == nullptr || args->o1 == nullptr) return SVA_ERR_INVALID_ARGUMENT;
+  const int64_t D = static_cast<int64_t>(args->H) * args->d;
+  const void* ptrs[5] = {grads->dout, grads->dq, grads->dk, grads->dv, grads->dgate};
+  const int64_t lds[5] = {grads->lddo, grads->lddq, grads->lddk, grads->lddv, grads->lddg};
+  if ((grads->dgate == nullptr) != (args->gate == nullptr)) return SVA_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 5; ++i) {
+    if (i == 4 && grads->dgate == nullptr) break;
+    if (ptrs[i] == nullptr || !aligned16(ptrs[i]) || !ld_ok(lds[i], D, args->dtype))
+      return SVA_ERR_INVALID_ARGUMENT;
+  }
+  if (grads->dlam == nullptr ||
+      reinterpret_cast<uintptr_t>(grads->dlam) % esize(args->dtype) != 0 ||
+      (args->ldl == 0 ? grads->lddl != 0 : grads->lddl < args->H))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (ws == nullptr || !aligned16(ws) ||
+      ws_bytes < sva_diff_anchor_bwd_workspace_bytes(args->B, args->N, args->H, args->d,
+                                                     args->n_keys, args->dtype))
+    return SVA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = clear_status(ws, s)) != SVA_OK) return st;
+  void* scratch = static_cast<char*>(ws) + SVA_STATUS_BYTES;
+  const cudaError_t e = diff_bwd_f32(*args, *grads, static_cast<int*>(ws), scratch, s);
+  return e == cudaSuccess ? SVA_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------------------
+// block norms
+// ---------------------------------------------------------------------------
+
+namespace {
+
+struct NormPtr {
+  const void* p;
+  int64_t ld;
+  sva_dtype_t dt;
+};
+bool norm_ptr_ok(const NormPtr& x, int64_t D) {
+  return x.p != nullptr && aligned16(x.p) && ld_ok(x.ld, D, x.dt);
+}
+
+sva_status_t check_norm(const sva_block_norm_args* a) {
+  if (a == nullptr) return SVA_ERR_INVALID_ARGUMENT;
+  if (a->dtype != SVA_F32 && a->dtype != SVA_BF16) return SVA_ERR_INVALID_ARGUMENT;
+  if (a->kind != SVA_NORM_RMS && a->kind != SVA_NORM_LAYER) return SVA_ERR_INVALID_ARGUMENT;
+  if (a->B < 1 || a->N < 1 || a->D < 1) return SVA_ERR_INVALID_ARGUMENT;
+  if (!(a->eps >= 0.f && std::isfinite(a->eps)) || !std::isfinite(a->res_scale))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (a->o == nullptr && a->u == nullptr) return SVA_ERR_INVALID_ARGUMENT;
+  if (a->o == nullptr && (a->w_post != nullptr || a->gate != nullptr))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (a->u == nullptr && (a->w_pre != nullptr || a->scale != nullptr || a->shift != nullptr))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (a->o != nullptr &&
+      (!norm_ptr_ok({a->o, a->ldo, a->dtype}, a->D) || !norm_ptr_ok({a->h_out, a->ldho, SVA_F32}, a->D)))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (a->u != nullptr && !norm_ptr_ok({a->u, a->ldu, a->dtype}, a->D))
+    return SVA_ERR_INVALID_ARGUMENT;
+  const NormPtr rows[3] = {{a->gate, a->ldgate, a->dtype},
+                           {a->scale, a->ldscale, a->dtype},
+                           {a->shift, a->ldshift, a->dtype}};
+  for (const NormPtr& x : rows)
+    if (x.p != nullptr && !norm_ptr_ok(x, a->D)) return SVA_ERR_INVALID_ARGUMENT;
+  if ((a->w_post != nullptr && !aligned16(a->w_post)) ||
+      (a->w_pre != nullptr && !aligned16(a->w_pre)) ||
+      (a->stats != nullptr && !aligned16(a->stats)))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (a->D > 8192 || static_cast<int64_t>(a->B) * a->N > INT32_MAX) return SVA_ERR_UNSUPPORTED;
+  return SVA_OK;
+}
+
+}  // namespace
+
+extern "C" sva_status_t sva_block_norm_fwd(const sva_block_norm_args* args, sva_stream_t stream) {
+  const sva_status_t st = check_norm(args);
+  if (st != SVA_OK) return st;
+  if (!norm_ptr_ok({args->h, args->ldh, SVA_F32}, args->D)) return SVA_ERR_INVALID_ARGUMENT;
+  const cudaError_t e = block_norm_fwd(*args, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SVA_OK : cuda_fail(e);
+}
+
+extern "C" size_t sva_block_norm_bwd_workspace_bytes(int B, int N, int D) {
+  if (B < 1 || N < 1 || D < 1) return 0;
+  return SVA_STATUS_BYTES + block_norm_partial_bytes(B, N, D);
+}
+
+extern "C" sva_status_t sva_block_norm_bwd(const sva_block_norm_args* args,
+                                           const sva_block_norm_grads* grads, void* ws,
+                                           size_t ws_bytes, sva_stream_t stream) {
+  sva_status_t st = check_norm(args);
+  if (st != SVA_OK) return st;
+  if (grads == nullptr || args->stats == nullptr) return SVA_ERR_INVALID_ARGUMENT;
+  const sva_block_norm_grads& g = *grads;
+  if (args->o == nullptr && !norm_ptr_ok({args->h, args->ldh, SVA_F32}, args->D))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (g.dh_out != nullptr && !norm_ptr_ok({g.dh_out, g.lddho, SVA_F32}, args->D))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (!norm_ptr_ok({g.dh, g.lddh, SVA_F32}, args->D)) return SVA_ERR_INVALID_ARGUMENT;
+  if (args->u != nullptr ? !norm_ptr_ok({g.du, g.lddu, args->dtype}, args->D)
+                         : (g.du != nullptr || g.dw_pre != nullptr || g.dscale != nullptr ||
+                            g.dshift != nullptr))
+    return SVA_ERR_INVALID_ARGUMENT;
+  if (args->o != nullptr ? !norm_ptr_ok({g.d_o, g.lddo, args->dtype}, args->D)
+                         : (g.d_o != nullptr || g.dw_post != nullptr || g.dgate != nullptr))
+    return SVA_ERR_INVALID_ARGUMENT;
+  const float* sums[5] = {g.dw_post, g.dgate, g.dw_pre, g.dscale, g.dshift};
+  for (const float* p : sums)
+    if (reinterpret_cast<uintptr_t>(p) & 3) return SVA_ERR_INVALID_ARGUMENT;
+  if (ws == nullptr || !aligned16(ws) ||
+      ws_bytes < sva_block_norm_bwd_workspace_bytes(args->B, args->N, args->D))
+    return SVA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = clear_status(ws, s)) != SVA_OK) return st;
+  const cudaError_t e = block_norm_bwd(*args, g, static_cast<char*>(ws) + SVA_STATUS_BYTES, s);
+  return e == cudaSuccess ? SVA_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------------------
 // projections
 // ---------------------------------------------------------------------------
 
