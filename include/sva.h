@@ -185,7 +185,8 @@ sva_status_t sva_softmax_anchor_fwd(const sva_attn_args* args, void* ws, size_t 
  * v hold (NaN and infinities too); a value outside [0, n_keys] is taken as the
  * nearer end. A batch with no key gives A = 0. All N query rows are computed.
  * Supported: SVA_BF16 with d = 128 (tcgen05 kernels), SVA_F32 with d in
- * {64, 128}. Any N >= 1 and n_keys >= 1.
+ * {64, 128}. Any N >= 1 and n_keys >= 1 with B*max(N, n_keys) and B*H*N below
+ * 2^31 and B*H at most 65,535.
  *
  * Training: give o1, o2 (fp32 [B, N, D], contiguous: the two maps' outputs
  * P_m V; in 32 bits, since dG and dlambda are made of them) and lse (fp32

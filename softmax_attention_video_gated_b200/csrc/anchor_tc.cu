@@ -94,17 +94,6 @@ struct AnchorTail {
 };
 constexpr size_t kAnchorSmem = 1024 + TAIL_OFF + sizeof(AnchorTail);
 
-__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
-  int never = 0;
-  return mbar_wait(bar, parity, &never, nullptr, 0);
-}
-
-__device__ __forceinline__ float ex2_mufu(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Work of one launch: units (query-tile pair, head, batch), x fastest. The
 // first n_full units run whole, one CTA each. The remaining units (the last,
 // partial wave) are split `split` ways along the key blocks. Each part writes

@@ -23,6 +23,8 @@ enum : int {
   WHERE_LIN_READOUT = 3,
   WHERE_ANCHOR = 4,
   WHERE_SELFTEST = 5,
+  WHERE_DIFF = 6,
+  WHERE_DIFF_BWD = 7,
 };
 
 // Default limit of one mbarrier wait. Every legitimate wait in these kernels
@@ -71,6 +73,14 @@ __device__ __forceinline__ float fast_tanh(float x) {
 }
 __device__ __forceinline__ float fast_sigmoid(float x) { return fmaf(0.5f, fast_tanh(0.5f * x), 0.5f); }
 
+// 2^x on the MUFU unit (about two units in the last place; results below the
+// normal range become zero)
+__device__ __forceinline__ float ex2_mufu(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float relu_f(float x) { return fmaxf(x, 0.0f); }
 
 // ReLU on 8 packed bf16 values (4 x bf16x2)
@@ -93,6 +103,11 @@ __device__ __forceinline__ void f2unpack(uint64_t v, float& a, float& b) {
 __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
@@ -213,6 +228,15 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       : "memory");
 }
 
+// untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned)
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1,
                                              int c2) {
   asm volatile(
@@ -298,6 +322,13 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Wait for `bar`, which is about to complete by itself (copies or MMAs in
+// flight at a CTA's end): no abort flag ends it early, the time limit does.
+__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
+  int never = 0;
+  return mbar_wait(bar, parity, &never, nullptr, 0);
 }
 
 // arrive once on `bar` when every tcgen05 op issued so far by this thread is done

@@ -1,0 +1,232 @@
+// diff_aux.cu -- around the differential anchor's attention core, for both types:
+// the launch plans, the merge of a key split, and the backward pass's
+// preparation. All of it is memory traffic.
+#include <algorithm>
+
+#include "diff_common.cuh"
+
+namespace sva {
+namespace {
+
+// Joins the parts of split units: per map, with M the largest part maximum and
+// w_p = 2^(m_p - M), O = sum w_p O_p and l = sum w_p l_p. One warp per query row.
+template <typename T>
+__global__ void __launch_bounds__(256) diff_merge_kernel(const sva_diff_args a, DiffWork wk,
+                                                         int n_split_units) {
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (wid >= static_cast<int64_t>(n_split_units) * wk.rows) return;
+  const int su = static_cast<int>(wid / wk.rows), r = static_cast<int>(wid % wk.rows);
+  const DiffUnit u = diff_unit(wk, wk.n_full + su * wk.split);
+  const int t = u.q0 + r;
+  if (t >= a.N) return;
+  float4 o[2];
+  float mx[2], l[2];
+#pragma unroll
+  for (int mm = 0; mm < 2; ++mm) {
+    mx[mm] = -INFINITY;
+    for (int p = 0; p < wk.split; ++p)
+      mx[mm] = fmaxf(mx[mm], diff_part(wk, a.d, su, p, mm)[wk.rows * a.d + 2 * r]);
+    o[mm] = make_float4(0.f, 0.f, 0.f, 0.f);
+    l[mm] = 0.f;
+    for (int p = 0; p < wk.split; ++p) {
+      const float* po = diff_part(wk, a.d, su, p, mm);
+      const float2 ml = *reinterpret_cast<const float2*>(po + wk.rows * a.d + 2 * r);
+      if (ml.x == -INFINITY) continue;  // a part without keys; its O is not written
+      const float w = exp2f(ml.x - mx[mm]);
+      if (4 * lane < a.d) {
+        const float4 x = *reinterpret_cast<const float4*>(po + r * a.d + 4 * lane);
+        o[mm].x = fmaf(w, x.x, o[mm].x);
+        o[mm].y = fmaf(w, x.y, o[mm].y);
+        o[mm].z = fmaf(w, x.z, o[mm].z);
+        o[mm].w = fmaf(w, x.w, o[mm].w);
+      }
+      l[mm] = fmaf(w, ml.y, l[mm]);
+    }
+  }
+  if (4 * lane < a.d)
+    finish4<T>(a, u.b, u.h, t, 4 * lane, o[0], o[1], l[0], l[1], lambda_of<T>(a, u.b, t, u.h));
+  if (lane == 0) {
+    finish_lse(a, 0, u.b, u.h, t, mx[0], l[0]);
+    finish_lse(a, 1, u.b, u.h, t, mx[1], l[1]);
+  }
+}
+
+// dA = dout sigmoid(G) (kept in dtype for the products that follow), dG, the
+// row sums delta_m = dA . O_m and dlambda = -delta_2. One warp per (token,
+// head), the tokens rounded up to whole tiles of 64: those behind the last
+// get a weight of zero. delta_m is made of the rounded dA, as dP is, so that
+// dP - delta_m cancels where a map sits on one key; dlambda is a result of its
+// own and is made of the unrounded one.
+template <typename T>
+__global__ void __launch_bounds__(256) diff_prep_kernel(const sva_diff_args a,
+                                                        const sva_diff_grads g, DiffBwdScratch ws) {
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const int n_tiles = (a.N + 63) / 64;
+  const int h = static_cast<int>(wid % a.H);
+  const int64_t prow = wid / a.H;
+  const int b = static_cast<int>(prow / (n_tiles * 64)), t = static_cast<int>(prow % (n_tiles * 64));
+  if (b >= a.B) return;
+  const int bh = b * a.H + h;
+  float* st = ws.stats + stat_at(bh, n_tiles, t);
+  if (t >= a.N) {
+    if (lane < kStats) st[lane * 64] = lane < 2 ? -INFINITY : 0.f;
+    return;
+  }
+  const int64_t row = static_cast<int64_t>(b) * a.N + t;
+  const float lam = lambda_of<T>(a, b, t, h);
+  float d1 = 0.f, d2 = 0.f, dl = 0.f;
+  if (4 * lane < a.d) {
+    const int col = h * a.d + 4 * lane;
+    const int64_t at = row * a.H * a.d + col;
+    const float4 o1 = load4<float>(a.o1 + at);
+    const float4 o2 = load4<float>(a.o2 + at);
+    float4 da = load4(static_cast<const T*>(g.dout) + row * g.lddo + col);
+    if (a.gate != nullptr) {
+      const float4 x = load4(static_cast<const T*>(a.gate) + row * a.ldg + col);
+      const float4 s = make_float4(sigmoid_f(x.x), sigmoid_f(x.y), sigmoid_f(x.z), sigmoid_f(x.w));
+      const float4 dg = make_float4(da.x * fmaf(-lam, o2.x, o1.x) * s.x * (1.f - s.x),
+                                    da.y * fmaf(-lam, o2.y, o1.y) * s.y * (1.f - s.y),
+                                    da.z * fmaf(-lam, o2.z, o1.z) * s.z * (1.f - s.z),
+                                    da.w * fmaf(-lam, o2.w, o1.w) * s.w * (1.f - s.w));
+      store4(static_cast<T*>(g.dgate) + row * g.lddg + col, dg);
+      da = make_float4(da.x * s.x, da.y * s.y, da.z * s.z, da.w * s.w);
+    }
+    dl = -dot4(da, o2);
+    da = round4(da, static_cast<const T*>(nullptr));
+    store4(static_cast<T*>(ws.da) + at, da);
+    d1 = dot4(da, o1);
+    d2 = dot4(da, o2);
+  }
+  d1 = warp_sum(d1);
+  d2 = warp_sum(d2);
+  dl = warp_sum(dl);
+  if (lane < 2) {
+    // an empty row's -infinity stays: its weights come out as 2^-inf = 0
+    const float lse = a.lse[(static_cast<int64_t>(lane) * a.B * a.H + bh) * a.N + t];
+    st[lane * 64] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    st[(2 + lane) * 64] = lane == 0 ? -d1 : -d2;
+  }
+  if (lane == 2) st[4 * 64] = -lam;
+  if (lane == 0) {
+    if (a.ldl != 0) {
+      const float f = (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : lam * (1.f - lam);
+      from_f32(static_cast<T*>(g.dlam) + row * g.lddl + h, dl * f);
+    } else {
+      ws.dlam[static_cast<int64_t>(bh) * a.N + t] = dl;
+    }
+  }
+}
+
+// dlam of a lambda shared by all tokens: one block per head
+template <typename T>
+__global__ void __launch_bounds__(1024) diff_dlam_kernel(const sva_diff_args a,
+                                                         const sva_diff_grads g,
+                                                         DiffBwdScratch ws) {
+  __shared__ float part[32];
+  const int h = blockIdx.x;
+  float s = 0.f;
+  for (int b = 0; b < a.B; ++b) {
+    const float* p = ws.dlam + (static_cast<int64_t>(b) * a.H + h) * a.N;
+    for (int t = threadIdx.x; t < a.N; t += blockDim.x) s += p[t];
+  }
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    s = part[threadIdx.x];
+    s = warp_sum(s);
+    if (threadIdx.x == 0) {
+      const float lam = lambda_of<T>(a, 0, 0, h);
+      const float f = (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : lam * (1.f - lam);
+      from_f32(static_cast<T*>(g.dlam) + h, s * f);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t prepare(const sva_diff_args& a, const sva_diff_grads& g, const DiffBwdScratch& ws,
+                    cudaStream_t s) {
+  const int64_t threads = static_cast<int64_t>(a.B) * ((a.N + 63) / 64 * 64) * a.H * 32;
+  diff_prep_kernel<T><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(a, g, ws);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.ldl != 0) return e;
+  diff_dlam_kernel<T><<<static_cast<unsigned>(a.H), 1024, 0, s>>>(a, g, ws);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt) {
+  DiffPlan p;
+  const bool tc = dt == SVA_BF16;
+  p.rows = tc ? kDiffTcRows : kDiffF32Rows;
+  const int keys = tc ? kDiffTcKeys : kDiffF32Keys;
+  const int Nk = n_keys > 0 ? n_keys : N;
+  p.n_qtiles = static_cast<int>((N + static_cast<int64_t>(p.rows) - 1) / p.rows);
+  const int64_t nkb = (Nk + static_cast<int64_t>(keys) - 1) / keys;
+  const int64_t units = static_cast<int64_t>(p.n_qtiles) * B * H;
+  const int64_t slots = static_cast<int64_t>(std::max(1, device_sm_count())) * (tc ? 1 : 2);
+  p.n_full = static_cast<int>(units);
+  // The last wave's units, cut s ways, take waves(s) x (their key blocks + 2
+  // blocks' time for a CTA's start and end), and one more such time for the
+  // merge. Cut them where that saves a fifth of the wave at least.
+  const int64_t tail = units % slots;
+  int64_t best = nkb + 2;
+  const int64_t most = best * 4 / 5;
+  for (int64_t sp = 2; tail > 0 && sp <= std::min<int64_t>(nkb, 32); ++sp) {
+    const int64_t cost = (tail * sp + slots - 1) / slots * ((nkb + sp - 1) / sp + 2) + 2;
+    if (cost < best && cost <= most) {
+      best = cost;
+      p.split = static_cast<int>(sp);
+    }
+  }
+  if (p.split > 1) {
+    p.n_split_units = static_cast<int>(tail);
+    p.n_full = static_cast<int>(units - tail);
+    p.partial_bytes = static_cast<size_t>(tail) * p.split * 2 * p.rows *
+                      (static_cast<size_t>(d) + 2) * sizeof(float);
+  }
+  return p;
+}
+
+cudaError_t diff_merge(const sva_diff_args& a, const DiffPlan& p, void* scratch, cudaStream_t s) {
+  if (p.n_split_units == 0) return cudaSuccess;
+  const DiffWork wk = diff_work(p, a.H, scratch);
+  const int64_t threads = static_cast<int64_t>(p.n_split_units) * p.rows * 32;
+  const unsigned grid = static_cast<unsigned>((threads + 255) / 256);
+  if (a.dtype == SVA_BF16)
+    diff_merge_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, wk, p.n_split_units);
+  else
+    diff_merge_kernel<float><<<grid, 256, 0, s>>>(a, wk, p.n_split_units);
+  return cudaGetLastError();
+}
+
+DiffBwdPlan diff_bwd_plan(int B, int N, int H, int d, sva_dtype_t dt) {
+  DiffBwdPlan p;
+  const size_t rows = static_cast<size_t>(B) * N;
+  const size_t tiles = static_cast<size_t>(B) * H * ((static_cast<size_t>(N) + 63) / 64);
+  p.stats_off = align_up(rows * H * d * (dt == SVA_BF16 ? 2 : 4), 256);
+  p.dlam_off = p.stats_off + tiles * kStats * 64 * sizeof(float);
+  p.total = p.dlam_off + rows * H * sizeof(float);
+  return p;
+}
+
+DiffBwdScratch diff_bwd_scratch(const sva_diff_args& a, void* scratch) {
+  const DiffBwdPlan p = diff_bwd_plan(a.B, a.N, a.H, a.d, a.dtype);
+  char* base = static_cast<char*>(scratch);
+  return {base, reinterpret_cast<float*>(base + p.stats_off),
+          reinterpret_cast<float*>(base + p.dlam_off)};
+}
+
+cudaError_t diff_bwd(const sva_diff_args& a, const sva_diff_grads& g, int* status, void* scratch,
+                     cudaStream_t s) {
+  const bool tc = a.dtype == SVA_BF16;
+  const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
+  const cudaError_t e = tc ? prepare<__nv_bfloat16>(a, g, ws, s) : prepare<float>(a, g, ws, s);
+  if (e != cudaSuccess) return e;
+  return tc ? diff_bwd_bf16(a, g, status, scratch, s) : diff_bwd_f32(a, g, scratch, s);
+}
+
+}  // namespace sva

@@ -1,0 +1,491 @@
+// diff_bwd_tc.cu -- gradients of the differential softmax anchor's products, bf16,
+// d = 128, on tcgen05/TMEM. With P_m recomputed from the saved log-sum-exp, dA
+// and the row sums delta_m (diff_aux.cu):
+//     W = P_1 - lambda P_2,  dS_1 = P_1 (dP - delta_1),  dS_2 = -lambda P_2 (dP - delta_2)
+//     dV = W^T dA,  dK_m = scale dS_m^T Q_m,  dQ_m = scale dS_m K_m
+// Two kernels of one shape, so that every output has one owner and its sum one
+// order (no atomics): 128 rows X, Y stand, blocks of 64 rows X', Y' stream by.
+//     keys stand:    X, Y = K, V   X', Y' = Q, dA   S^T = K Q^T, dP^T = V dA^T;
+//                    out dK = dS^T Q, dV = W^T dA
+//     queries stand: X, Y = Q, dA  X', Y' = K, V    S = Q K^T, dP = dA V^T; out dQ = dS K
+// Either recomputes the scores: 7/5 of the products of one pass over the pairs,
+// against adding dQ into memory in an order that changes from run to run.
+//
+// 12 warps in three warpgroups: warp 0 TMA, warp 1 TMEM and every MMA, WG1 and
+// WG2 the weights: thread r of either owns standing row r (its TMEM lane) and 32
+// of the block's 64 columns. W and dS go back to TMEM in bf16 as A operands of the
+// products; dS over dP, W beside. The next block's scores are issued as soon as
+// the threads hold this block's in registers.
+#include <algorithm>
+
+#include "diff_common.cuh"
+
+namespace sva {
+namespace {
+
+constexpr int HD = 128;
+constexpr int BR = 128, BS = 64;
+constexpr int BOXR = 64 * BR * 2;  // [64 columns x 128 rows] bf16
+constexpr int BOXS = 64 * BS * 2;  // [64 columns x 64 rows]
+constexpr int STAGES = 4;
+constexpr int STAGE_BYTES = 4 * BOXS;  // X', Y'
+constexpr int STAT_BYTES = kStats * 64 * 4;
+constexpr int NUM_THREADS = 384;
+constexpr int TMEM_COLS = 512;
+constexpr int kRegsProducer = 56, kRegsWeights = 224;
+// TMEM columns
+constexpr int TM_S = 0;      // S_1, S_2: 64 each
+constexpr int TM_DP = 128;   // dP, then dS_1, dS_2
+constexpr int TM_W = 192;    // keys stand: W, two buffers of 32
+constexpr int TM_X = 192;    // queries stand: Q and dA as A operands, 64 each
+constexpr int TM_ACC = 256;  // keys stand: dK, dV
+constexpr int TM_ACCQ = 384; // queries stand: dQ
+
+struct Tail {
+  uint64_t x_full;
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t s_full, s_empty, dp_full, w_full, ds_full;
+  uint64_t acc_done;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+template <bool KV>
+struct Layout {
+  static constexpr int X_OFF = 0;  // keys stand: K, V, two boxes each
+  static constexpr int RING = KV ? 4 * BOXR : 0;
+  static constexpr int STAT = RING + STAGES * STAGE_BYTES;
+  static constexpr int TAIL = STAT + (KV ? STAGES * STAT_BYTES : 0);
+  static constexpr size_t SMEM = 1024 + TAIL + sizeof(Tail);
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
+};
+
+template <bool KV>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    diff_bwd_tc_kernel(const __grid_constant__ CUtensorMap map_x,
+                       const __grid_constant__ CUtensorMap map_y,
+                       const __grid_constant__ CUtensorMap map_x2,
+                       const __grid_constant__ CUtensorMap map_y2,
+                       const __grid_constant__ sva_diff_args a,
+                       const __grid_constant__ sva_diff_grads g, DiffBwdScratch ws, int n_tiles,
+                       float scale, int* status) {
+  using L = Layout<KV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Tail* tl = reinterpret_cast<Tail*>(smem + L::TAIL);
+  const int tile = static_cast<int>(blockIdx.x) % n_tiles;
+  const int bh = static_cast<int>(blockIdx.x) / n_tiles;
+  const int h = bh % a.H, b = bh / a.H;
+  const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
+  const int valid = key_count(a.key_lens, b, Nk);
+  const int r0 = tile * BR;
+  const int n_stat_tiles = (a.N + 63) / 64;
+  const int n = KV ? (r0 < valid ? n_stat_tiles : 0) : (valid + BS - 1) / BS;
+  const float scale_log2 = scale * kLog2e;
+  const int warp = warp_id(), lane = lane_id();
+  const int wg = warp >> 2;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&tl->x_full, KV ? 1 : 256);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&tl->full[s], 1);
+      mbar_init(&tl->empty[s], 1);
+    }
+    mbar_init(&tl->s_full, 1);
+    mbar_init(&tl->s_empty, 256);
+    mbar_init(&tl->dp_full, 1);
+    mbar_init(&tl->w_full, 256);
+    mbar_init(&tl->ds_full, 256);
+    mbar_init(&tl->acc_done, 1);
+    mbar_init(&tl->drain, 1);
+    tl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tl->tmem_base, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tl->tmem_base;
+  volatile int* abort_flag = &tl->abort_flag;
+
+  if (wg == 0) {
+    warpgroup_reg_dec<kRegsProducer>();
+    if (warp == 0) {
+      // ------------------------------------------------ TMA producer
+      if (KV && n > 0 && lane == 0) {
+        mbar_arrive_expect_tx(&tl->x_full, 4 * BOXR);
+        tma_load_3d(&map_x, &tl->x_full, smem + L::X_OFF, h * HD, r0, b);
+        tma_load_3d(&map_x, &tl->x_full, smem + L::X_OFF + BOXR, h * HD + 64, r0, b);
+        tma_load_3d(&map_y, &tl->x_full, smem + L::X_OFF + 2 * BOXR, h * HD, r0, b);
+        tma_load_3d(&map_y, &tl->x_full, smem + L::X_OFF + 3 * BOXR, h * HD + 64, r0, b);
+      }
+      __syncwarp();
+      int issued = 0;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        const int st = j % STAGES;
+        const bool w = mbar_wait(&tl->empty[st], ((j / STAGES) & 1) ^ 1, abort_flag, status,
+                                 WHERE_DIFF_BWD);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          uint8_t* p = smem + L::RING + st * STAGE_BYTES;
+          mbar_arrive_expect_tx(&tl->full[st], STAGE_BYTES + (KV ? STAT_BYTES : 0));
+          tma_load_3d(&map_x2, &tl->full[st], p, h * HD, j * BS, b);
+          tma_load_3d(&map_x2, &tl->full[st], p + BOXS, h * HD + 64, j * BS, b);
+          tma_load_3d(&map_y2, &tl->full[st], p + 2 * BOXS, h * HD, j * BS, b);
+          tma_load_3d(&map_y2, &tl->full[st], p + 3 * BOXS, h * HD + 64, j * BS, b);
+          if (KV)
+            bulk_load(smem + L::STAT + st * STAT_BYTES, ws.stats + stat_at(bh, n_stat_tiles, j * BS),
+                      STAT_BYTES, &tl->full[st]);
+        }
+        __syncwarp();
+        ++issued;
+      }
+      if (lane == 0) {
+        if (KV && n > 0) (void)drain_wait(&tl->x_full, 0);
+        if (!ok)
+          for (int i = max(0, issued - STAGES); i < issued; ++i)
+            (void)drain_wait(&tl->full[i % STAGES], (i / STAGES) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc_s = idesc_bf16_f32(BR, BS, false, false);      // X X'^T
+      constexpr uint32_t idesc_half = idesc_bf16_f32(BR, HD / 2, false, true);  // dS_m X'_m
+      constexpr uint32_t idesc_full = idesc_bf16_f32(BR, HD, false, true);      // W Y'
+      const uint64_t xd = smem_desc(smem_u32(smem + L::X_OFF), 16, 1024);
+      const uint64_t sk = smem_desc(smem_u32(smem + L::RING), 16, 1024);      // K-major
+      const uint64_t sm = smem_desc(smem_u32(smem + L::RING), BOXS, 1024);    // MN-major
+      // S_1, S_2 of the block in stage st: 64 of the 128 columns each
+      auto issue_s = [&](int st) {
+        const uint64_t bb = sk + static_cast<uint64_t>(st * (STAGE_BYTES >> 4));
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const int m = kk >> 2, e = kk & 3;
+          const uint64_t bd = bb + ((m * BOXS + e * 32) >> 4);
+          const uint32_t d = tmem + TM_S + 64 * m;
+          if (KV)
+            umma_ss(d, xd + ((m * BOXR + e * 32) >> 4), bd, idesc_s, e != 0 ? 1u : 0u);
+          else
+            umma_ts(d, tmem + TM_X + 8 * kk, bd, idesc_s, e != 0 ? 1u : 0u);
+        }
+        umma_commit(&tl->s_full);
+      };
+      auto issue_dp = [&](int st) {
+        const uint64_t bb = sk + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint64_t bd = bb + (((kk >> 2) * BOXS + (kk & 3) * 32) >> 4);
+          if (KV)
+            umma_ss(tmem + TM_DP, xd + ((2 * BOXR + (kk >> 2) * BOXR + (kk & 3) * 32) >> 4), bd,
+                    idesc_s, kk != 0 ? 1u : 0u);
+          else
+            umma_ts(tmem + TM_DP, tmem + TM_X + 64 + 8 * kk, bd, idesc_s, kk != 0 ? 1u : 0u);
+        }
+        umma_commit(&tl->dp_full);
+      };
+      // queries stand: the last block's rows of K behind the batch's last key
+      // become zero, since a weight of zero times what lies there may be NaN
+      auto stage_ready = [&](int j) -> bool {
+        const int st = j % STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait(&tl->full[st], (j / STAGES) & 1, abort_flag, status,
+                                               WHERE_DIFF_BWD)))
+          return false;
+        const int left = valid - j * BS;
+        if (!KV && left < BS && valid < Nk) {
+          uint8_t* p = smem + L::RING + st * STAGE_BYTES;
+          for (int i = left * 8 + lane; i < BS * 8; i += 32) {
+            *reinterpret_cast<uint4*>(p + i * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(p + BOXS + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        return true;
+      };
+      bool ok = true;
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&tl->x_full, 0, abort_flag, status, WHERE_DIFF_BWD)) &&
+             stage_ready(0);
+        if (ok && lane == 0) {
+          issue_s(0);
+          issue_dp(0);
+        }
+        __syncwarp();
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int st = j % STAGES, sn = (j + 1) % STAGES;
+        const bool more = j + 1 < n;
+        if (more) {
+          ok = stage_ready(j + 1) &&
+               __all_sync(0xffffffffu,
+                          mbar_wait(&tl->s_empty, j & 1, abort_flag, status, WHERE_DIFF_BWD));
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) issue_s(sn);
+          __syncwarp();
+        }
+        if (KV) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&tl->w_full, j & 1, abort_flag, status, WHERE_DIFF_BWD));
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t yb = sm + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < BS / 16; ++kk)
+              umma_ts(tmem + TM_ACC + HD, tmem + TM_W + 32 * (j & 1) + 8 * kk,
+                      yb + (kk * 2048 >> 4), idesc_full, (kk != 0 || j != 0) ? 1u : 0u);
+          }
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&tl->ds_full, j & 1, abort_flag, status, WHERE_DIFF_BWD));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t xb = sm + static_cast<uint64_t>(st * (STAGE_BYTES >> 4));
+          // 16 columns of dS_m: those of warpgroup kk >> 1, beside its share of the other map
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int kk = 0; kk < BS / 16; ++kk)
+              umma_ts(tmem + (KV ? TM_ACC : TM_ACCQ) + 64 * m,
+                      tmem + TM_DP + 32 * (kk >> 1) + 16 * m + 8 * (kk & 1),
+                      xb + ((m * BOXS + kk * 2048) >> 4), idesc_half,
+                      (kk != 0 || j != 0) ? 1u : 0u);
+          umma_commit(&tl->empty[st]);
+          if (more) issue_dp(sn);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) {
+        if (ok) umma_commit(&tl->acc_done);
+        umma_commit(&tl->drain);
+        (void)drain_wait(&tl->drain, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    warpgroup_reg_inc<kRegsWeights>();
+    // ------------------------------------------------ weights, then the results
+    const int half = wg - 1;  // this warpgroup's 32 of the block's 64 columns
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int row = r0 + r;
+    const int n_rows = KV ? Nk : a.N;
+    const uint64_t scale2 = f2pack(scale_log2, scale_log2);
+    uint64_t nlse1 = 0, nlse2 = 0, nd1 = 0, nd2 = 0, nl = 0;  // queries stand: this row's
+    if (!KV && n > 0) {
+      const bool in = row < a.N;
+      uint32_t x[32];
+      const uint4* src =
+          half == 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                     (static_cast<int64_t>(b) * a.N + row) * a.ldq + h * HD)
+                    : reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(ws.da) +
+                                                     (static_cast<int64_t>(b) * a.N + row) * a.H * HD + h * HD);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 w = in ? src[8 * c + i] : make_uint4(0, 0, 0, 0);
+          x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
+        }
+        tmem_st32(lane_base + TM_X + 64 * half + 32 * c, x);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&tl->x_full);
+      // rows behind the last query: their -infinity makes every weight zero
+      const float* st = ws.stats + stat_at(bh, n_stat_tiles, min(row, n_stat_tiles * 64 - 1));
+      const float f[5] = {in ? st[0] : -INFINITY, in ? st[64] : -INFINITY, st[128], st[192], st[256]};
+      nlse1 = f2pack(f[0], f[0]);
+      nlse2 = f2pack(f[1], f[1]);
+      nd1 = f2pack(f[2], f[2]);
+      nd2 = f2pack(f[3], f[3]);
+      nl = f2pack(f[4], f[4]);
+    }
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const float* stat = reinterpret_cast<const float*>(smem + L::STAT + (j % STAGES) * STAT_BYTES) +
+                          32 * half;
+      // the stage's statistics landed before the scores were made of its rows, but this
+      // thread has to see that copy itself
+      bool w = !KV || mbar_wait(&tl->full[j % STAGES], (j / STAGES) & 1, abort_flag, status,
+                                WHERE_DIFF_BWD);
+      w = w && mbar_wait(&tl->s_full, j & 1, abort_flag, status, WHERE_DIFF_BWD);
+      if (!__all_sync(0xffffffffu, w)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t s1[32], s2[32];
+      tmem_ld32(lane_base + TM_S + 32 * half, s1);
+      tmem_ld32(lane_base + TM_S + 64 + 32 * half, s2);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(&tl->s_empty);
+      uint64_t p1[16], q2[16];  // P_1 and -lambda P_2
+      uint32_t wk[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (KV) {
+          nlse1 = *reinterpret_cast<const uint64_t*>(stat + 2 * i);
+          nlse2 = *reinterpret_cast<const uint64_t*>(stat + 64 + 2 * i);
+          nl = *reinterpret_cast<const uint64_t*>(stat + 256 + 2 * i);
+        }
+        float x0, x1, y0, y1;
+        f2unpack(fma_f2(f2pack(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])), scale2,
+                        nlse1), x0, x1);
+        f2unpack(fma_f2(f2pack(__uint_as_float(s2[2 * i]), __uint_as_float(s2[2 * i + 1])), scale2,
+                        nlse2), y0, y1);
+        p1[i] = f2pack(ex2_mufu(x0), ex2_mufu(x1));
+        q2[i] = mul_f2(f2pack(ex2_mufu(y0), ex2_mufu(y1)), nl);
+        if (KV) {
+          float w0, w1;
+          f2unpack(add_f2(p1[i], q2[i]), w0, w1);
+          wk[i] = pack_bf16x2(w0, w1);
+        }
+      }
+      if (KV) {
+        tmem_st16(lane_base + TM_W + 32 * (j & 1) + 16 * half, wk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&tl->w_full);
+      }
+      w = mbar_wait(&tl->dp_full, j & 1, abort_flag, status, WHERE_DIFF_BWD);
+      if (!__all_sync(0xffffffffu, w)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t dp[32], d1[16], d2[16];
+      tmem_ld32(lane_base + TM_DP + 32 * half, dp);
+      tmem_wait_ld();
+      const int left = valid - j * BS - 32 * half;  // queries stand: keys that count
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (KV) {
+          nd1 = *reinterpret_cast<const uint64_t*>(stat + 128 + 2 * i);
+          nd2 = *reinterpret_cast<const uint64_t*>(stat + 192 + 2 * i);
+        }
+        const uint64_t dpp = f2pack(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
+        float x0, x1, y0, y1;
+        f2unpack(mul_f2(p1[i], add_f2(dpp, nd1)), x0, x1);
+        f2unpack(mul_f2(q2[i], add_f2(dpp, nd2)), y0, y1);
+        d1[i] = pack_bf16x2(x0, x1);
+        d2[i] = pack_bf16x2(y0, y1);
+      }
+      if (!KV && left < 32) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t keep = (2 * i < left ? 0xFFFFu : 0u) | (2 * i + 1 < left ? 0xFFFF0000u : 0u);
+          d1[i] &= keep;
+          d2[i] &= keep;
+        }
+      }
+      tmem_st16(lane_base + TM_DP + 32 * half, d1);
+      tmem_st16(lane_base + TM_DP + 32 * half + 16, d2);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&tl->ds_full);
+    }
+    if (ok && n > 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(&tl->acc_done, 0, abort_flag, status, WHERE_DIFF_BWD));
+    tc_fence_after();
+    // keys stand: WG1 writes dK, WG2 dV, all 128 columns; queries stand: half of dQ each
+    const int64_t at = static_cast<int64_t>(b) * n_rows + row;
+    __nv_bfloat16* dst;
+    int col0, ncols;
+    float f;
+    if (KV) {
+      dst = half == 0 ? static_cast<__nv_bfloat16*>(g.dk) + at * g.lddk
+                      : static_cast<__nv_bfloat16*>(g.dv) + at * g.lddv;
+      col0 = TM_ACC + HD * half;
+      ncols = HD;
+      f = half == 0 ? scale : 1.0f;
+    } else {
+      dst = static_cast<__nv_bfloat16*>(g.dq) + at * g.lddq + 64 * half;
+      col0 = TM_ACCQ + 64 * half;
+      ncols = 64;
+      f = scale;
+    }
+    dst += h * HD;
+    const bool zero = n == 0 || (KV && row >= valid);
+#pragma unroll 1
+    for (int c = 0; c < ncols && ok; c += 32) {
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld32(lane_base + col0 + c, o);
+        tmem_wait_ld();
+      }
+      if (row >= n_rows) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (!zero) {
+          v.x = pack_bf16x2(f * __uint_as_float(o[8 * k]), f * __uint_as_float(o[8 * k + 1]));
+          v.y = pack_bf16x2(f * __uint_as_float(o[8 * k + 2]), f * __uint_as_float(o[8 * k + 3]));
+          v.z = pack_bf16x2(f * __uint_as_float(o[8 * k + 4]), f * __uint_as_float(o[8 * k + 5]));
+          v.w = pack_bf16x2(f * __uint_as_float(o[8 * k + 6]), f * __uint_as_float(o[8 * k + 7]));
+        }
+        *reinterpret_cast<uint4*>(dst + c + 8 * k) = v;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+template <bool KV>
+cudaError_t launch(const sva_diff_args& a, const sva_diff_grads& g, const DiffBwdScratch& ws,
+                   float scale, int* status, cudaStream_t s) {
+  const int D = a.H * a.d;
+  const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
+  CUtensorMap mx, my, mx2, my2;
+  bool ok;
+  if (KV) {
+    ok = diff_map(&mx, a.k, a.ldk, a.B, Nk, D, BR) && diff_map(&my, a.v, a.ldv, a.B, Nk, D, BR) &&
+         diff_map(&mx2, a.q, a.ldq, a.B, a.N, D, BS) && diff_map(&my2, ws.da, D, a.B, a.N, D, BS);
+  } else {
+    ok = diff_map(&mx2, a.k, a.ldk, a.B, Nk, D, BS) && diff_map(&my2, a.v, a.ldv, a.B, Nk, D, BS);
+    mx = mx2;  // Q and dA go to TMEM by the threads' own loads
+    my = my2;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  const int n_tiles = ((KV ? Nk : a.N) + BR - 1) / BR;
+  auto kern = diff_bwd_tc_kernel<KV>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(Layout<KV>::SMEM));
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(n_tiles * a.B * a.H), NUM_THREADS, Layout<KV>::SMEM, s>>>(
+      mx, my, mx2, my2, a, g, ws, n_tiles, scale, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t diff_bwd_bf16(const sva_diff_args& a, const sva_diff_grads& g, int* status,
+                          void* scratch, cudaStream_t s) {
+  const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
+  const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(HD / 2));
+  const cudaError_t e = launch<true>(a, g, ws, scale, status, s);
+  return e != cudaSuccess ? e : launch<false>(a, g, ws, scale, status, s);
+}
+
+}  // namespace sva

@@ -1,0 +1,149 @@
+// diff_common.cuh -- what the kernels of the differential softmax anchor share:
+// element access, lambda and key counts, the end of a query row, and the layout
+// of the backward pass's scratch.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace sva {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
+
+// fp32 to a few units in the last place: the gate meets fp32 results too
+__device__ __forceinline__ float sigmoid_f(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+__device__ __forceinline__ int key_count(const int32_t* key_lens, int b, int Nk) {
+  return key_lens == nullptr ? Nk : max(0, min(Nk, key_lens[b]));
+}
+
+// lambda of token t (batch b, head h)
+template <typename T>
+__device__ __forceinline__ float lambda_of(const sva_diff_args& a, int b, int64_t t, int h) {
+  const T* p = static_cast<const T*>(a.lam);
+  const float x = to_f32(a.ldl == 0 ? p[h] : p[(static_cast<int64_t>(b) * a.N + t) * a.ldl + h]);
+  return (a.flags & SVA_FLAG_LAMBDA_VALUE) ? x : sigmoid_f(x);
+}
+
+// One query row's end: both maps normalised, lambda, gate, stores, saved tensors.
+// o1, o2: this thread's four columns [c, c + 4) of the head (unnormalised).
+template <typename T>
+__device__ __forceinline__ void finish4(const sva_diff_args& a, int b, int h, int64_t t, int c,
+                                        float4 o1, float4 o2, float l1, float l2, float lam) {
+  const float i1 = l1 > 0.f ? 1.0f / l1 : 0.f, i2 = l2 > 0.f ? 1.0f / l2 : 0.f;
+  o1 = make_float4(o1.x * i1, o1.y * i1, o1.z * i1, o1.w * i1);
+  o2 = make_float4(o2.x * i2, o2.y * i2, o2.z * i2, o2.w * i2);
+  const int64_t row = static_cast<int64_t>(b) * a.N + t;
+  const int col = h * a.d + c;
+  if (a.o1 != nullptr) {
+    const int64_t at = row * a.H * a.d + col;
+    store4(a.o1 + at, o1);
+    store4(a.o2 + at, o2);
+  }
+  float4 y = make_float4(fmaf(-lam, o2.x, o1.x), fmaf(-lam, o2.y, o1.y), fmaf(-lam, o2.z, o1.z),
+                         fmaf(-lam, o2.w, o1.w));
+  if (a.gate != nullptr) {
+    const float4 g = load4(static_cast<const T*>(a.gate) + row * a.ldg + col);
+    y = make_float4(y.x * sigmoid_f(g.x), y.y * sigmoid_f(g.y), y.z * sigmoid_f(g.z),
+                    y.w * sigmoid_f(g.w));
+  }
+  store4(static_cast<T*>(a.out) + row * a.ldo + col, y);
+}
+
+__device__ __forceinline__ void finish_lse(const sva_diff_args& a, int m, int b, int h, int64_t t,
+                                           float mx, float l) {
+  if (a.lse != nullptr)
+    a.lse[((static_cast<int64_t>(m) * a.B + b) * a.H + h) * a.N + t] =
+        l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+constexpr int kStats = 5;
+__device__ __forceinline__ int64_t stat_at(int bh, int n_tiles, int t) {
+  return (static_cast<int64_t>(bh) * n_tiles + (t >> 6)) * (kStats * 64) + (t & 63);
+}
+
+__device__ __forceinline__ float4 round4(float4 v, const float*) { return v; }
+__device__ __forceinline__ float4 round4(float4 v, const __nv_bfloat16*) {
+  const uint32_t a = pack_bf16x2(v.x, v.y), b = pack_bf16x2(v.z, v.w);
+  return make_float4(bf16lo_to_f32(a), bf16hi_to_f32(a), bf16lo_to_f32(b), bf16hi_to_f32(b));
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b) {
+  return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Tensor map of a bf16 activation [B, N, D] (row stride ld): boxes of 64
+// columns (one 128-byte swizzle row) x `rows` tokens; what lies outside is zero.
+inline bool diff_map(CUtensorMap* m, const void* base, int64_t ld, int B, int N, int D, int rows) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(N),
+                            static_cast<uint64_t>(B)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(ld) * 2,
+                               static_cast<uint64_t>(ld) * 2 * static_cast<uint64_t>(N)};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(rows), 1};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Work of one forward launch: units (query tile, head, batch), tiles fastest.
+// The first n_full run whole, one CTA each; the rest, the last partial wave, are
+// cut `split` ways along the key blocks, and every part leaves both maps'
+// unnormalised output and (running maximum in log2 units, sum) per row.
+struct DiffWork {
+  int n_qtiles, H, rows, n_full, split;
+  float* partial;  // [unit][part][map][rows x d O | rows x (m, l)]
+};
+__host__ __device__ inline DiffWork diff_work(const DiffPlan& p, int H, void* scratch) {
+  return {p.n_qtiles, H, p.rows, p.n_full, p.split, static_cast<float*>(scratch)};
+}
+struct DiffUnit {
+  int q0, h, b, part, su;  // part < 0: the unit runs whole
+};
+__device__ __forceinline__ DiffUnit diff_unit(const DiffWork& wk, int cta) {
+  DiffUnit u;
+  int unit = cta;
+  u.part = -1;
+  u.su = 0;
+  if (cta >= wk.n_full) {
+    u.su = (cta - wk.n_full) / wk.split;
+    u.part = (cta - wk.n_full) % wk.split;
+    unit = wk.n_full + u.su;
+  }
+  u.q0 = (unit % wk.n_qtiles) * wk.rows;
+  u.h = (unit / wk.n_qtiles) % wk.H;
+  u.b = unit / wk.n_qtiles / wk.H;
+  return u;
+}
+__device__ __forceinline__ float* diff_part(const DiffWork& wk, int d, int su, int part, int map) {
+  return wk.partial +
+         ((static_cast<int64_t>(su) * wk.split + part) * 2 + map) * wk.rows * (d + 2);
+}
+
+}  // namespace
+}  // namespace sva

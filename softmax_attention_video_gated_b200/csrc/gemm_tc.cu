@@ -89,11 +89,6 @@ __device__ __forceinline__ void tma_store_wait_read1() {
   asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
-__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
-  int never = 0;
-  return mbar_wait(bar, parity, &never, nullptr, 0);
-}
-
 // MMA width of an N tile: the full BN, or for the ragged last tile its width
 // rounded up to 32 (a legal N for M = 256 on a CTA pair), so a narrow tail
 // costs tensor-core time in proportion to its width

@@ -119,25 +119,37 @@ cudaError_t anchor_bf16(const sva_attn_args& a, int* status, void* scratch, cuda
 cudaError_t anchor_f32(const sva_attn_args& a, int* status, cudaStream_t s);
 
 // ---------------------------------------------------------------- differential anchor
-// Key split of a forward call: the keys of every (batch, head, query tile) are
-// cut into `split` runs of key blocks; with split > 1 each part leaves its two
-// maps' unnormalised outputs, running maxima and sums in scratch and a merge
-// kernel joins them.
+constexpr int kDiffTcRows = 128, kDiffTcKeys = 128;  // bf16: query rows and keys of a tile
+constexpr int kDiffF32Rows = 32, kDiffF32Keys = 32;
+// Units (query tile, head, batch) of a forward call; those of the last partial
+// wave may be cut `split` ways along the keys, with parts in scratch.
 struct DiffPlan {
-  int rows = 0, keys = 0;        // tile: query rows, keys of one block
-  int n_qtiles = 0, n_kblocks = 0, split = 1;
+  int rows = 0, n_qtiles = 0, n_full = 0, n_split_units = 0, split = 1;
   size_t partial_bytes = 0;
+  unsigned grid() const { return static_cast<unsigned>(n_full + n_split_units * split); }
 };
 DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt);
-cudaError_t diff_fwd_f32(const sva_diff_args& a, int* status, void* scratch, cudaStream_t s);
+cudaError_t diff_fwd_f32(const sva_diff_args& a, void* scratch, cudaStream_t s);
+cudaError_t diff_fwd_bf16(const sva_diff_args& a, int* status, void* scratch, cudaStream_t s);
+cudaError_t diff_merge(const sva_diff_args& a, const DiffPlan& p, void* scratch, cudaStream_t s);
 // Scratch of a backward call: dA (dtype, [B*N, D]), then the queries' statistics
 // (per batch, head and 64-query tile) and dlambda per token (fp32).
 struct DiffBwdPlan {
   size_t stats_off = 0, dlam_off = 0, total = 0;
 };
+struct DiffBwdScratch {
+  void* da;      // [B, N, D] in dtype
+  float* stats;  // [B*H][tiles of 64 queries][5][64]: -lse_m log2 e, -delta_m, -lambda
+  float* dlam;   // [B*H][N]: dlambda per token, where one lambda is shared by all
+};
 DiffBwdPlan diff_bwd_plan(int B, int N, int H, int d, sva_dtype_t dt);
-cudaError_t diff_bwd_f32(const sva_diff_args& a, const sva_diff_grads& g, int* status,
-                         void* scratch, cudaStream_t s);
+DiffBwdScratch diff_bwd_scratch(const sva_diff_args& a, void* scratch);
+cudaError_t diff_bwd(const sva_diff_args& a, const sva_diff_grads& g, int* status, void* scratch,
+                     cudaStream_t s);
+cudaError_t diff_bwd_f32(const sva_diff_args& a, const sva_diff_grads& g, void* scratch,
+                         cudaStream_t s);
+cudaError_t diff_bwd_bf16(const sva_diff_args& a, const sva_diff_grads& g, int* status,
+                          void* scratch, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms
 size_t block_norm_partial_bytes(int B, int N, int D);

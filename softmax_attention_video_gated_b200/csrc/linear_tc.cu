@@ -60,11 +60,6 @@ struct StateTail {
 };
 constexpr size_t kStateSmem = 1024 + ST_STAGES * ST_STAGE_BYTES + sizeof(StateTail);
 
-__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
-  int never = 0;
-  return mbar_wait(bar, parity, &never, nullptr, 0);
-}
-
 // kWriteGate: token t's row of phi(K) is scaled by omega_t = sigmoid(wgate[b, t, h])
 // before it enters S and z (the write-gated variant); wgate is [B, N, >=H], row
 // stride ldw.

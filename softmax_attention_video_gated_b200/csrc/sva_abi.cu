@@ -268,7 +268,8 @@ sva_status_t check_diff(const sva_diff_args* a) {
               (reinterpret_cast<uintptr_t>(a->lse) & 3)))
     return SVA_ERR_INVALID_ARGUMENT;
   if (static_cast<int64_t>(a->B) * std::max(a->N, a->n_keys) > INT32_MAX ||
-      static_cast<int64_t>(a->B) * a->H > 65535)
+      static_cast<int64_t>(a->B) * a->H > 65535 ||
+      static_cast<int64_t>(a->B) * a->H > INT32_MAX / a->N)
     return SVA_ERR_UNSUPPORTED;
   if (a->dtype == SVA_BF16 && a->d != 128) return SVA_ERR_UNSUPPORTED;
   if (a->dtype == SVA_F32 && a->d != 64 && a->d != 128) return SVA_ERR_UNSUPPORTED;
@@ -302,7 +303,9 @@ extern "C" sva_status_t sva_diff_anchor_fwd(const sva_diff_args* args, void* ws,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((st = clear_status(ws, s)) != SVA_OK) return st;
   void* scratch = static_cast<char*>(ws) + SVA_STATUS_BYTES;
-  const cudaError_t e = diff_fwd_f32(*args, static_cast<int*>(ws), scratch, s);
+  const cudaError_t e = args->dtype == SVA_BF16
+                            ? diff_fwd_bf16(*args, static_cast<int*>(ws), scratch, s)
+                            : diff_fwd_f32(*args, scratch, s);
   return e == cudaSuccess ? SVA_OK : cuda_fail(e);
 }
 
@@ -337,7 +340,7 @@ extern "C" sva_status_t sva_diff_anchor_bwd(const sva_diff_args* args, const sva
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((st = clear_status(ws, s)) != SVA_OK) return st;
   void* scratch = static_cast<char*>(ws) + SVA_STATUS_BYTES;
-  const cudaError_t e = diff_bwd_f32(*args, *grads, static_cast<int*>(ws), scratch, s);
+  const cudaError_t e = diff_bwd(*args, *grads, static_cast<int*>(ws), scratch, s);
   return e == cudaSuccess ? SVA_OK : cuda_fail(e);
 }
 
