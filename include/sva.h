@@ -255,7 +255,7 @@ sva_status_t sva_diff_anchor_bwd(const sva_diff_args* args, const sva_diff_grads
  * used without it; it may alias h. w_post, w_pre ([D]), gate, scale, shift
  * ([B, >=D], one row per batch) are in dtype and nullable (1, 1, 1, 0, 0).
  * Modulation per frame: pass B * frames as B. h and h' are fp32. Statistics
- * and sums are fp32. 1 <= D <= 8192; B * N < 2^31.
+ * and sums are fp32. 1 <= D <= 8192; B * N < 2^31, B at most 65,535.
  *
  * Training: give stats (fp32 [B*N][4], 16-byte aligned) to the forward call and
  * to sva_block_norm_bwd, which takes dh_out (the gradient of h', fp32, nullable

@@ -152,9 +152,9 @@ cudaError_t diff_bwd_bf16(const sva_diff_args& a, const sva_diff_grads& g, int* 
                           void* scratch, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms
-size_t block_norm_partial_bytes(int B, int N, int D);
+size_t block_norm_scratch_bytes(int B, int N, int D);
 cudaError_t block_norm_fwd(const sva_block_norm_args& a, cudaStream_t s);
-cudaError_t block_norm_bwd(const sva_block_norm_args& a, const sva_block_norm_grads& g,
+cudaError_t block_norm_bwd(const sva_block_norm_args& a, const sva_block_norm_grads& g, int* status,
                            void* scratch, cudaStream_t s);
 
 // ---------------------------------------------------------------- router

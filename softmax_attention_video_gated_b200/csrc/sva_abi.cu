@@ -385,7 +385,7 @@ sva_status_t check_norm(const sva_block_norm_args* a) {
       (a->w_pre != nullptr && !aligned16(a->w_pre)) ||
       (a->stats != nullptr && !aligned16(a->stats)))
     return SVA_ERR_INVALID_ARGUMENT;
-  if (a->D > 8192 || static_cast<int64_t>(a->B) * a->N > INT32_MAX) return SVA_ERR_UNSUPPORTED;
+  if (a->D > 8192 || static_cast<int64_t>(a->B) * a->N > INT32_MAX || a->B > 65535) return SVA_ERR_UNSUPPORTED;
   return SVA_OK;
 }
 
@@ -401,7 +401,7 @@ extern "C" sva_status_t sva_block_norm_fwd(const sva_block_norm_args* args, sva_
 
 extern "C" size_t sva_block_norm_bwd_workspace_bytes(int B, int N, int D) {
   if (B < 1 || N < 1 || D < 1) return 0;
-  return SVA_STATUS_BYTES + block_norm_partial_bytes(B, N, D);
+  return SVA_STATUS_BYTES + block_norm_scratch_bytes(B, N, D);
 }
 
 extern "C" sva_status_t sva_block_norm_bwd(const sva_block_norm_args* args,
@@ -430,8 +430,9 @@ extern "C" sva_status_t sva_block_norm_bwd(const sva_block_norm_args* args,
       ws_bytes < sva_block_norm_bwd_workspace_bytes(args->B, args->N, args->D))
     return SVA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = clear_status(ws, s)) != SVA_OK) return st;
-  const cudaError_t e = block_norm_bwd(*args, g, static_cast<char*>(ws) + SVA_STATUS_BYTES, s);
+  // the kernel waits for nothing and reports nothing: it writes the status words itself
+  const cudaError_t e = block_norm_bwd(*args, g, static_cast<int*>(ws),
+                                       static_cast<char*>(ws) + SVA_STATUS_BYTES, s);
   return e == cudaSuccess ? SVA_OK : cuda_fail(e);
 }
 
