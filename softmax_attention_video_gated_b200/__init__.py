@@ -384,68 +384,97 @@ def sva_softmax_anchor_fwd(q, k, v, gate, out, H: int, residual=None, scale: flo
     return ws
 
 
-def _same_dtype(dt, **tensors):
-    for name, t in tensors.items():
-        if t is not None and _dtype_code(t) != dt:
-            raise TypeError(f"{name} must have the dtype of the call's activations")
+# The calls below are also made for a handful of tokens, where the time to check
+# and pack their arguments is the call's time: each tensor is looked at once, and
+# the structs are filled in one go, in the order of their fields.
+
+_NULL = (None, 0)
 
 
-def _width(t, W: int, name: str):
-    if t.shape[-1] < W:
-        raise ValueError(f"{name} must be at least {W} wide, got {tuple(t.shape)}")
-
-
-def _lam_stride(lam, B: int, N: int, H: int, name: str) -> int:
-    """Row stride of per-token lambdas [B, N, >=H]; 0 for the shared form [H]."""
-    if not lam.is_cuda:
+def _lead(t):
+    """(dtype, its code, device index) of a call, from its leading tensor; the kernels run on the
+    current device."""
+    dev = t.get_device()
+    torch = _torch()
+    if dev < 0:
         raise ValueError("expected a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+    return t.dtype, _dtype_code(t), dev
+
+
+def _here(stream, dev: int) -> int:
+    """The call's stream: the given one, or the current one of its device."""
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(dev)
+
+
+def _act(t, B: int, N: int, W: int, dt, dev: int, name: str):
+    """(address, row stride) of an activation [B, N, >=W]; (None, 0) for None."""
+    if t is None:
+        return _NULL
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != B or shape[1] != N or shape[2] < W:
+        raise ValueError(f"expected {name} [B={B}, N={N}, >={W}], got {tuple(shape)}")
+    # a single row's stride is not used: a rounded one keeps it valid for odd widths
+    ld = stride[1] if N > 1 else stride[0] if B > 1 else (max(stride[1], W) + 7) // 8 * 8
+    if (stride[2] != 1 and W > 1) or (B > 1 and stride[0] != N * ld):
+        raise ValueError(f"{name}: rows must be unit-stride with batches N*ld apart")
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    return t.data_ptr(), ld
+
+
+def _flat(t, shape: tuple, dt, dev: int, name: str):
+    """Address of a contiguous tensor of this shape; None for None."""
+    if t is None:
+        return None
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"expected {name} contiguous {shape}, got {tuple(t.shape)}")
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _lam(lam, B: int, N: int, H: int, dt, dev: int, name: str):
+    """(address, row stride) of per-token lambdas [B, N, >=H]; stride 0 for the shared form [H]."""
     if lam.dim() == 1:
-        if lam.shape[0] != H or lam.stride(0) != 1:
-            raise ValueError(f"expected {name} [H={H}] contiguous, got {tuple(lam.shape)}")
-        return 0
-    ld = _rows(lam, B, N)
-    _width(lam, H, name)
-    return ld
+        return _flat(lam, (H,), dt, dev, name), 0
+    return _act(lam, B, N, H, dt, dev, name)
 
 
-def _diff_args(q, k, v, gate, lam, out, H, key_lens, scale, flags, saved) -> DiffArgs:
+def _space(ws, need, dev: int):
+    """The call's workspace, made to measure where none is given."""
+    if ws is None:
+        return workspace(need(), f"cuda:{dev}")
+    if ws.get_device() != dev:
+        raise ValueError(f"ws must be on cuda:{dev}")
+    return ws
+
+
+def _diff_args(q, k, v, gate, lam, out, H, key_lens, scale, flags, saved):
     torch = _torch()
     B, N, D = q.shape
     Nk = k.shape[1]
-    if D % H:
+    if H < 1 or D % H:
         raise ValueError(f"width {D} is not a multiple of H={H}")
-    dt = _dtype_code(q)
-    _same_dtype(dt, k=k, v=v, gate=gate, lam=lam, out=out)
-    a = DiffArgs()
-    a.B, a.N, a.H, a.d, a.dtype = B, N, H, D // H, dt
-    a.n_keys = Nk if Nk != N else 0
-    a.q, a.ldq = _ptr(q), _rows(q, B, N)
-    a.k, a.ldk = _ptr(k), _rows(k, B, Nk)
-    a.v, a.ldv = _ptr(v), _rows(v, B, Nk)
-    for name, t in (("k", k), ("v", v), ("gate", gate), ("out", out)):
-        if t is not None:
-            _width(t, D, name)
-    if gate is not None:
-        a.gate, a.ldg = _ptr(gate), _rows(gate, B, N)
-    a.lam, a.ldl = _ptr(lam), _lam_stride(lam, B, N, H, "lam")
-    if key_lens is not None:
-        if key_lens.dtype != torch.int32 or key_lens.shape != (B,) or not key_lens.is_contiguous() \
-                or not key_lens.is_cuda:
-            raise ValueError(f"key_lens must be a contiguous int32 CUDA tensor of {B} values")
-        a.key_lens = _ptr(key_lens)
-    if out is not None:
-        a.out, a.ldo = _ptr(out), _rows(out, B, N)
-    a.scale, a.flags = float(scale), int(flags)
+    dt, code, dev = _lead(q)
+    if key_lens is not None and key_lens.dtype is not torch.int32:
+        raise ValueError(f"key_lens must be int32, got {key_lens.dtype}")
+    lens = _flat(key_lens, (B,), torch.int32, dev, "key_lens")
+    o1 = o2 = lse = None
     if saved is not None:
-        o1, o2, lse = saved
-        for t, shape in ((o1, (B, N, D)), (o2, (B, N, D)), (lse, (2, B, H, N))):
-            if tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError("saved must be contiguous CUDA tensors o1, o2 [B, N, D] and "
-                                 f"lse [2, B, H, N], got {tuple(t.shape)}")
-            if t.dtype != torch.float32:
-                raise TypeError("saved tensors must be float32")
-        a.o1, a.o2, a.lse = _ptr(o1), _ptr(o2), _ptr(lse)
-    return a
+        f32 = torch.float32
+        o1, o2 = (_flat(t, (B, N, D), f32, dev, "saved") for t in saved[:2])
+        lse = _flat(saved[2], (2, B, H, N), f32, dev, "saved")
+    return DiffArgs(B, N, H, D // H, Nk if Nk != N else 0, code,
+                    *_act(q, B, N, D, dt, dev, "q"), *_act(k, B, Nk, D, dt, dev, "k"),
+                    *_act(v, B, Nk, D, dt, dev, "v"), *_act(gate, B, N, D, dt, dev, "gate"),
+                    *_lam(lam, B, N, H, dt, dev, "lam"), lens, *_act(out, B, N, D, dt, dev, "out"),
+                    scale, flags, o1, o2, lse), dev
 
 
 def sva_diff_anchor_workspace_bytes(B: int, N: int, H: int, d: int, n_keys: int, dtype: int) -> int:
@@ -458,11 +487,9 @@ def sva_diff_anchor_fwd(q, k, v, gate, lam, out, H: int, key_lens=None, scale: f
     queries and keys being the halves of each head's columns. gate may be None. lam: logits
     [B, N, >=H] or [H] (lambda itself with SVA_FLAG_LAMBDA_VALUE). key_lens [B] int32: keys
     of each batch. saved (o1, o2, lse): written for sva_diff_anchor_bwd."""
-    a = _diff_args(q, k, v, gate, lam, out, H, key_lens, scale, flags, saved)
-    if ws is None:
-        ws = workspace(sva_diff_anchor_workspace_bytes(a.B, a.N, a.H, a.d, a.n_keys, a.dtype),
-                       q.device)
-    _check(_lib().sva_diff_anchor_fwd(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)),
+    a, dev = _diff_args(q, k, v, gate, lam, out, H, key_lens, scale, flags, saved)
+    ws = _space(ws, lambda: sva_diff_anchor_workspace_bytes(a.B, a.N, a.H, a.d, a.n_keys, a.dtype), dev)
+    _check(_lib().sva_diff_anchor_fwd(ctypes.byref(a), ws.data_ptr(), ws.numel(), _here(stream, dev)),
            "sva_diff_anchor_fwd")
     return ws
 
@@ -478,65 +505,52 @@ def sva_diff_anchor_bwd(q, k, v, gate, lam, dout, saved, dq, dk, dv, dgate, dlam
     None exactly when gate is; dlam is laid out as lam."""
     if saved is None:
         raise ValueError("the backward pass needs the forward pass's saved (o1, o2, lse)")
-    a = _diff_args(q, k, v, gate, lam, None, H, key_lens, scale, flags, saved)
-    D, Nk = a.H * a.d, k.shape[1]
-    _same_dtype(a.dtype, dout=dout, dq=dq, dk=dk, dv=dv, dgate=dgate, dlam=dlam)
-    g = DiffGrads()
-    for name, t, n in (("dout", dout, a.N), ("dq", dq, a.N), ("dk", dk, Nk), ("dv", dv, Nk),
-                       ("dgate", dgate, a.N)):
-        if t is not None:
-            _width(t, D, name)
-            setattr(g, name, _ptr(t))
-            setattr(g, {"dout": "lddo", "dgate": "lddg"}.get(name, "ld" + name), _rows(t, a.B, n))
-    g.dlam, g.lddl = _ptr(dlam), _lam_stride(dlam, a.B, a.N, a.H, "dlam")
-    if ws is None:
-        ws = workspace(sva_diff_anchor_bwd_workspace_bytes(a.B, a.N, a.H, a.d, a.n_keys, a.dtype),
-                       q.device)
-    _check(_lib().sva_diff_anchor_bwd(ctypes.byref(a), ctypes.byref(g), _ptr(ws), ws.numel(),
-                                      _stream(stream)), "sva_diff_anchor_bwd")
+    a, dev = _diff_args(q, k, v, gate, lam, None, H, key_lens, scale, flags, saved)
+    B, N, D = q.shape
+    Nk, dt = k.shape[1], q.dtype
+    g = DiffGrads(*_act(dout, B, N, D, dt, dev, "dout"), *_act(dq, B, N, D, dt, dev, "dq"),
+                  *_act(dk, B, Nk, D, dt, dev, "dk"), *_act(dv, B, Nk, D, dt, dev, "dv"),
+                  *_act(dgate, B, N, D, dt, dev, "dgate"), *_lam(dlam, B, N, H, dt, dev, "dlam"))
+    ws = _space(ws, lambda: sva_diff_anchor_bwd_workspace_bytes(B, N, H, a.d, a.n_keys, a.dtype), dev)
+    _check(_lib().sva_diff_anchor_bwd(ctypes.byref(a), ctypes.byref(g), ws.data_ptr(), ws.numel(),
+                                      _here(stream, dev)), "sva_diff_anchor_bwd")
     return ws
 
 
-def _batch_rows(t, B: int, D: int, name: str):
-    """Row stride of a per-batch modulation [B, >=D]."""
-    if t.dim() != 2 or t.shape[0] != B or t.stride(1) != 1 or not t.is_cuda:
-        raise ValueError(f"expected a CUDA tensor {name} [B={B}, >={D}] of unit-stride rows, "
-                         f"got {tuple(t.shape)}")
-    _width(t, D, name)
-    return t.stride(0) if B > 1 else max(t.stride(0), D)
+def _batch_rows(t, B: int, D: int, dt, dev: int, name: str):
+    """(address, row stride) of a per-batch modulation [B, >=D]; (None, 0) for None."""
+    if t is None:
+        return _NULL
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != B or shape[1] < D or (stride[1] != 1 and D > 1):
+        raise ValueError(f"expected {name} [B={B}, >={D}] of unit-stride rows, got {tuple(shape)}")
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if B > 1:
+        return t.data_ptr(), stride[0]
+    # one row: any stride does, a rounded one keeps it valid for odd widths
+    return t.data_ptr(), (D + 7) // 8 * 8
 
 
-def _norm_args(h, o, w_post, gate, h_out, w_pre, scale, shift, u, kind, eps, res_scale,
-               stats, dtype_of) -> BlockNormArgs:
-    torch = _torch()
+def _norm_args(h, o, w_post, gate, h_out, w_pre, scale, shift, u, kind, eps, res_scale, stats):
+    f32 = _torch().float32
+    like = o if o is not None else u
+    if like is None:
+        raise ValueError("one of o and u (forward) or du (backward) is needed")
     B, N, D = h.shape
-    a = BlockNormArgs()
-    a.B, a.N, a.D, a.dtype = B, N, D, _dtype_code(dtype_of)
-    a.kind, a.eps, a.res_scale = int(kind), float(eps), float(res_scale)
-    _same_dtype(a.dtype, o=o, w_post=w_post, gate=gate, w_pre=w_pre, scale=scale, shift=shift, u=u)
-    for name, t, ld in (("h", h, "ldh"), ("h_out", h_out, "ldho"), ("o", o, "ldo"), ("u", u, "ldu")):
-        if t is None:
-            continue
-        if name in ("h", "h_out") and t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32")
-        _width(t, D, name)
-        setattr(a, name, _ptr(t))
-        setattr(a, ld, _rows(t, B, N))
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        if t is not None:
-            if tuple(t.shape) != (D,) or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"expected a contiguous CUDA tensor {name} [D={D}]")
-            setattr(a, name, _ptr(t))
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is not None:
-            setattr(a, name, _ptr(t))
-            setattr(a, "ld" + name, _batch_rows(t, B, D, name))
-    if stats is not None:
-        if stats.dtype != torch.float32 or not stats.is_contiguous() or not stats.is_cuda \
-                or stats.numel() < 4 * B * N:
-            raise ValueError("stats must be a contiguous float32 CUDA tensor of 4 values per token")
-        a.stats = _ptr(stats)
-    return a
+    dt, code, dev = _lead(like)
+    return BlockNormArgs(B, N, D, code, kind, eps, res_scale,
+                         *_act(h, B, N, D, f32, dev, "h"), *_act(o, B, N, D, dt, dev, "o"),
+                         _flat(w_post, (D,), dt, dev, "w_post"),
+                         *_batch_rows(gate, B, D, dt, dev, "gate"),
+                         *_act(h_out, B, N, D, f32, dev, "h_out"),
+                         _flat(w_pre, (D,), dt, dev, "w_pre"),
+                         *_batch_rows(scale, B, D, dt, dev, "scale"),
+                         *_batch_rows(shift, B, D, dt, dev, "shift"),
+                         *_act(u, B, N, D, dt, dev, "u"),
+                         _flat(stats, (B, N, 4), f32, dev, "stats")), dev
 
 
 def sva_block_norm_fwd(h, o=None, w_post=None, gate=None, h_out=None, w_pre=None, scale=None,
@@ -546,12 +560,8 @@ def sva_block_norm_fwd(h, o=None, w_post=None, gate=None, h_out=None, w_pre=None
     (1 + scale) + shift (with u). h, h_out fp32 [B, N, D]; o, u [B, N, D]; weights [D];
     gate, scale, shift one row per batch [B, D]; stats [B, N, 4] fp32: written for
     sva_block_norm_bwd."""
-    dtype_of = o if o is not None else u
-    if dtype_of is None:
-        raise ValueError("one of o and u is needed")
-    a = _norm_args(h, o, w_post, gate, h_out, w_pre, scale, shift, u, kind, eps, res_scale, stats,
-                   dtype_of)
-    _check(_lib().sva_block_norm_fwd(ctypes.byref(a), _stream(stream)), "sva_block_norm_fwd")
+    a, dev = _norm_args(h, o, w_post, gate, h_out, w_pre, scale, shift, u, kind, eps, res_scale, stats)
+    _check(_lib().sva_block_norm_fwd(ctypes.byref(a), _here(stream, dev)), "sva_block_norm_fwd")
 
 
 def sva_block_norm_bwd_workspace_bytes(B: int, N: int, D: int) -> int:
@@ -565,37 +575,19 @@ def sva_block_norm_bwd(h_out, stats, dh, dh_out=None, o=None, do=None, du=None, 
     """Gradients of sva_block_norm_fwd. h_out: its result (h in a call without o); stats: as it
     wrote them; dh_out, du: the gradients of h_out and u. Writes dh, do and the sums over
     tokens dw_post, dw_pre [D] and dgate, dscale, dshift [B, D] (fp32) that are given."""
-    torch = _torch()
-    dtype_of = o if o is not None else du
-    if dtype_of is None:
-        raise ValueError("one of o and du is needed")
     # u takes part only by being there: du stands in its place
-    a = _norm_args(h_out, o, w_post, gate, h_out if o is not None else None, w_pre, scale, None, du,
-                   kind, eps, res_scale, stats, dtype_of)
+    a, dev = _norm_args(h_out, o, w_post, gate, h_out if o is not None else None, w_pre, scale, None, du,
+                        kind, eps, res_scale, stats)
     B, N, D = h_out.shape
-    g = BlockNormGrads()
-    _same_dtype(a.dtype, do=do, du=du)
-    for name, t, ld in (("dh_out", dh_out, "lddho"), ("du", du, "lddu"), ("dh", dh, "lddh"),
-                        ("d_o", do, "lddo")):
-        if t is None:
-            continue
-        if name in ("dh_out", "dh") and t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32")
-        _width(t, D, name)
-        setattr(g, name, _ptr(t))
-        setattr(g, ld, _rows(t, B, N))
-    for name, t, shape in (("dw_post", dw_post, (D,)), ("dgate", dgate, (B, D)),
-                           ("dw_pre", dw_pre, (D,)), ("dscale", dscale, (B, D)),
-                           ("dshift", dshift, (B, D))):
-        if t is not None:
-            if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() \
-                    or not t.is_cuda:
-                raise ValueError(f"{name} must be a contiguous float32 CUDA tensor {shape}")
-            setattr(g, name, _ptr(t))
-    if ws is None:
-        ws = workspace(sva_block_norm_bwd_workspace_bytes(B, N, D), h_out.device)
-    _check(_lib().sva_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), _ptr(ws), ws.numel(),
-                                     _stream(stream)), "sva_block_norm_bwd")
+    f32, dt = h_out.dtype, (o if o is not None else du).dtype
+    g = BlockNormGrads(*_act(dh_out, B, N, D, f32, dev, "dh_out"), *_act(du, B, N, D, dt, dev, "du"),
+                       *_act(dh, B, N, D, f32, dev, "dh"), *_act(do, B, N, D, dt, dev, "do"),
+                       _flat(dw_post, (D,), f32, dev, "dw_post"), _flat(dgate, (B, D), f32, dev, "dgate"),
+                       _flat(dw_pre, (D,), f32, dev, "dw_pre"), _flat(dscale, (B, D), f32, dev, "dscale"),
+                       _flat(dshift, (B, D), f32, dev, "dshift"))
+    ws = _space(ws, lambda: sva_block_norm_bwd_workspace_bytes(B, N, D), dev)
+    _check(_lib().sva_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), ws.data_ptr(), ws.numel(),
+                                     _here(stream, dev)), "sva_block_norm_bwd")
     return ws
 
 

@@ -685,11 +685,11 @@ RowRuns fwd_runs(const sva_block_norm_args& a) {
 // by sizes and type alone, whichever of the arrays a call has
 RowRuns bwd_runs(int B, int N, int D, int e) { return row_runs(B, N, D, 12, 12, 2, 8 + 2 * e); }
 
-template <typename K>
-cudaError_t launch(K kern, const RowRuns& rr, int smem, cudaStream_t s, void** args) {
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <auto K>
+cudaError_t launch(const RowRuns& rr, int smem, cudaStream_t s, void** args) {
+  const cudaError_t e = allow_max_smem<K>();
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernel(reinterpret_cast<const void*>(kern), dim3(static_cast<unsigned>(rr.total)),
+  return cudaLaunchKernel(reinterpret_cast<const void*>(K), dim3(static_cast<unsigned>(rr.total)),
                           dim3(static_cast<unsigned>(32 * rr.W * rr.groups)), args,
                           static_cast<size_t>(smem), s);
 }
@@ -702,10 +702,10 @@ cudaError_t launch_fwd(sva_block_norm_args a, cudaStream_t s) {
   const int smem = rr.groups * static_cast<int>(sizeof(GroupSums)) + width * 12 +
                    rr.groups * rr.stages * width * bytes;
   void* args[] = {&a, &rr};
-  if (nq == 1) return launch(norm_fwd_kernel<T, 1, 256>, rr, smem, s, args);
-  if (nq == 2) return launch(norm_fwd_kernel<T, 2, 256>, rr, smem, s, args);
-  if (rr.W <= 8) return launch(norm_fwd_kernel<T, 4, 256>, rr, smem, s, args);
-  return launch(norm_fwd_kernel<T, 4, 512>, rr, smem, s, args);
+  if (nq == 1) return launch<norm_fwd_kernel<T, 1, 256>>(rr, smem, s, args);
+  if (nq == 2) return launch<norm_fwd_kernel<T, 2, 256>>(rr, smem, s, args);
+  if (rr.W <= 8) return launch<norm_fwd_kernel<T, 4, 256>>(rr, smem, s, args);
+  return launch<norm_fwd_kernel<T, 4, 512>>(rr, smem, s, args);
 }
 
 // Scratch of a backward call: the CTAs' column sums, the batches' weighted sums,
@@ -741,13 +741,13 @@ cudaError_t launch_bwd(sva_block_norm_args a, sva_block_norm_grads g, bool sums,
   void* args[] = {&a, &g, &rr, &partial, &done, &status};
   cudaError_t err;
   if (nq == 1)
-    err = launch(norm_bwd_kernel<T, 1, 384>, rr, smem, s, args);
+    err = launch<norm_bwd_kernel<T, 1, 384>>(rr, smem, s, args);
   else if (nq == 2)
-    err = launch(norm_bwd_kernel<T, 2, 384>, rr, smem, s, args);
+    err = launch<norm_bwd_kernel<T, 2, 384>>(rr, smem, s, args);
   else if (rr.W <= 12)
-    err = launch(norm_bwd_kernel<T, 4, 384>, rr, smem, s, args);
+    err = launch<norm_bwd_kernel<T, 4, 384>>(rr, smem, s, args);
   else
-    err = launch(norm_bwd_kernel<T, 4, 512>, rr, smem, s, args);
+    err = launch<norm_bwd_kernel<T, 4, 512>>(rr, smem, s, args);
   if (err != cudaSuccess || !sums) return err;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

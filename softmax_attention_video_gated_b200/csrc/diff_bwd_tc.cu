@@ -58,7 +58,7 @@ struct Layout {
   static constexpr int STAT = RING + STAGES * STAGE_BYTES;
   static constexpr int TAIL = STAT + (KV ? STAGES * STAT_BYTES : 0);
   static constexpr size_t SMEM = 1024 + TAIL + sizeof(Tail);
-  static_assert(SMEM <= 232448, "shared memory of one CTA");
+  static_assert(SMEM <= kMaxSmem, "shared memory of one CTA");
 };
 
 template <bool KV>
@@ -469,11 +469,9 @@ cudaError_t launch(const sva_diff_args& a, const sva_diff_grads& g, const DiffBw
   }
   if (!ok) return cudaErrorInvalidValue;
   const int n_tiles = ((KV ? Nk : a.N) + BR - 1) / BR;
-  auto kern = diff_bwd_tc_kernel<KV>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(Layout<KV>::SMEM));
+  const cudaError_t e = allow_max_smem<diff_bwd_tc_kernel<KV>>();
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(n_tiles * a.B * a.H), NUM_THREADS, Layout<KV>::SMEM, s>>>(
+  diff_bwd_tc_kernel<KV><<<static_cast<unsigned>(n_tiles * a.B * a.H), NUM_THREADS, Layout<KV>::SMEM, s>>>(
       mx, my, mx2, my2, a, g, ws, n_tiles, scale, status);
   return cudaGetLastError();
 }

@@ -326,11 +326,9 @@ cudaError_t fwd(const sva_diff_args& a, void* scratch, cudaStream_t s) {
   const DiffPlan p = diff_plan(a.B, a.N, a.H, a.d, a.n_keys, a.dtype);
   const DiffWork wk = diff_work(p, a.H, scratch);
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
-  auto kern = diff_fwd_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(fwd_smem<D>()));
+  cudaError_t e = allow_max_smem<diff_fwd_kernel<D>>();
   if (e != cudaSuccess) return e;
-  kern<<<p.grid(), 128, fwd_smem<D>(), s>>>(a, scale * kLog2e, wk);
+  diff_fwd_kernel<D><<<p.grid(), 128, fwd_smem<D>(), s>>>(a, scale * kLog2e, wk);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return diff_merge(a, p, scratch, s);
 }
@@ -341,15 +339,13 @@ cudaError_t bwd(const sva_diff_args& a, const sva_diff_grads& g, void* scratch, 
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const unsigned bh = static_cast<unsigned>(a.B * a.H);
-  auto kq = diff_bwd_kernel<D, false>;
-  auto kk = diff_bwd_kernel<D, true>;
   const int smem = static_cast<int>(bwd_smem<D>());
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+  if ((e = allow_max_smem<diff_bwd_kernel<D, false>>()) != cudaSuccess ||
+      (e = allow_max_smem<diff_bwd_kernel<D, true>>()) != cudaSuccess)
     return e;
-  kq<<<dim3(static_cast<unsigned>((a.N + BR - 1) / BR), bh), 256, smem, s>>>(a, g, ws, scale);
-  kk<<<dim3(static_cast<unsigned>((Nk + BR - 1) / BR), bh), 256, smem, s>>>(a, g, ws, scale);
+  diff_bwd_kernel<D, false><<<dim3(static_cast<unsigned>((a.N + BR - 1) / BR), bh), 256, smem, s>>>(a, g, ws, scale);
+  diff_bwd_kernel<D, true><<<dim3(static_cast<unsigned>((Nk + BR - 1) / BR), bh), 256, smem, s>>>(a, g, ws, scale);
   return cudaGetLastError();
 }
 

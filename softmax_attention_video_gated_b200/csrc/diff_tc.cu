@@ -55,7 +55,7 @@ struct Tail {
   int abort_flag;
 };
 constexpr size_t kSmem = 1024 + TAIL_OFF + sizeof(Tail);
-static_assert(kSmem <= 232448, "shared memory of one CTA");
+static_assert(kSmem <= kMaxSmem, "shared memory of one CTA");
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     diff_tc_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -497,8 +497,7 @@ cudaError_t diff_fwd_bf16(const sva_diff_args& a, int* status, void* scratch, cu
     return cudaErrorInvalidValue;
   const DiffPlan p = diff_plan(a.B, a.N, a.H, a.d, a.n_keys, a.dtype);
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(HD / 2));
-  cudaError_t e = cudaFuncSetAttribute(diff_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmem));
+  cudaError_t e = allow_max_smem<diff_tc_kernel>();
   if (e != cudaSuccess) return e;
   diff_tc_kernel<<<p.grid(), NUM_THREADS, kSmem, s>>>(mq, mk, mv, mg, a, scale * kLog2e,
                                                       diff_work(p, a.H, scratch), status);

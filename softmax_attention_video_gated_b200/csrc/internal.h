@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/sva.h"
 
 namespace sva {
@@ -56,6 +58,18 @@ int device_index();
 bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base,
                  const uint64_t* dims, const uint64_t* strides_bytes /* rank-1 */,
                  const uint32_t* box, CUtensorMapSwizzle swizzle);
+
+// Lets kernel K have as much shared memory as a CTA can take, once per device.
+constexpr int kMaxSmem = 227 * 1024;
+template <auto K>
+cudaError_t allow_max_smem() {
+  static std::atomic<bool> done[64];
+  const int d = device_index();
+  if (d >= 0 && d < 64 && done[d].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess && d >= 0 && d < 64) done[d].store(true, std::memory_order_relaxed);
+  return e;
+}
 
 constexpr size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
