@@ -31,6 +31,7 @@ constexpr int STAGES = 4;
 constexpr int STAGE_BYTES = 4 * BOXS;  // X', Y'
 constexpr int STAT_BYTES = kStats * 64 * 4;
 constexpr int NUM_THREADS = 384;
+constexpr int kWarps = 8;  // that make weights; each arrives once for its 32 rows
 constexpr int TMEM_COLS = 512;
 constexpr int kRegsProducer = 56, kRegsWeights = 224;
 // TMEM columns
@@ -88,16 +89,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int wg = warp >> 2;
 
   if (threadIdx.x == 0) {
-    mbar_init(&tl->x_full, KV ? 1 : 256);
+    mbar_init(&tl->x_full, KV ? 1 : kWarps);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&tl->full[s], 1);
       mbar_init(&tl->empty[s], 1);
     }
     mbar_init(&tl->s_full, 1);
-    mbar_init(&tl->s_empty, 256);
+    mbar_init(&tl->s_empty, kWarps);
     mbar_init(&tl->dp_full, 1);
-    mbar_init(&tl->w_full, 256);
-    mbar_init(&tl->ds_full, 256);
+    mbar_init(&tl->w_full, kWarps);
+    mbar_init(&tl->ds_full, kWarps);
     mbar_init(&tl->acc_done, 1);
     mbar_init(&tl->drain, 1);
     tl->abort_flag = 0;
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&tl->x_full);
+      warp_arrive(&tl->x_full);
       // rows behind the last query: their -infinity makes every weight zero
       const float* st = ws.stats + stat_at(bh, n_stat_tiles, min(row, n_stat_tiles * 64 - 1));
       const float f[5] = {in ? st[0] : -INFINITY, in ? st[64] : -INFINITY, st[128], st[192], st[256]};
@@ -334,15 +335,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tmem_ld32(lane_base + TM_S + 64 + 32 * half, s2);
       tmem_wait_ld();
       tc_fence_before();
-      mbar_arrive(&tl->s_empty);
+      warp_arrive(&tl->s_empty);
       uint64_t p1[16], q2[16];  // P_1 and -lambda P_2
       uint32_t wk[16];
+      ulonglong2 f1, f2, f3;  // two pairs of queries' statistics at a time
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (KV) {
-          nlse1 = *reinterpret_cast<const uint64_t*>(stat + 2 * i);
-          nlse2 = *reinterpret_cast<const uint64_t*>(stat + 64 + 2 * i);
-          nl = *reinterpret_cast<const uint64_t*>(stat + 256 + 2 * i);
+          if (i % 2 == 0) {
+            f1 = *reinterpret_cast<const ulonglong2*>(stat + 2 * i);
+            f2 = *reinterpret_cast<const ulonglong2*>(stat + 64 + 2 * i);
+            f3 = *reinterpret_cast<const ulonglong2*>(stat + 256 + 2 * i);
+          }
+          nlse1 = i % 2 == 0 ? f1.x : f1.y;
+          nlse2 = i % 2 == 0 ? f2.x : f2.y;
+          nl = i % 2 == 0 ? f3.x : f3.y;
         }
         float x0, x1, y0, y1;
         f2unpack(fma_f2(f2pack(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])), scale2,
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_st16(lane_base + TM_W + 32 * (j & 1) + 16 * half, wk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&tl->w_full);
+        warp_arrive(&tl->w_full);
       }
       w = mbar_wait(&tl->dp_full, j & 1, abort_flag, status, WHERE_DIFF_BWD);
       if (!__all_sync(0xffffffffu, w)) {
@@ -376,8 +383,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (KV) {
-          nd1 = *reinterpret_cast<const uint64_t*>(stat + 128 + 2 * i);
-          nd2 = *reinterpret_cast<const uint64_t*>(stat + 192 + 2 * i);
+          if (i % 2 == 0) {
+            f1 = *reinterpret_cast<const ulonglong2*>(stat + 128 + 2 * i);
+            f2 = *reinterpret_cast<const ulonglong2*>(stat + 192 + 2 * i);
+          }
+          nd1 = i % 2 == 0 ? f1.x : f1.y;
+          nd2 = i % 2 == 0 ? f2.x : f2.y;
         }
         const uint64_t dpp = f2pack(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
         float x0, x1, y0, y1;
@@ -398,7 +409,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tmem_st16(lane_base + TM_DP + 32 * half + 16, d2);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&tl->ds_full);
+      warp_arrive(&tl->ds_full);
     }
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(&tl->acc_done, 0, abort_flag, status, WHERE_DIFF_BWD));

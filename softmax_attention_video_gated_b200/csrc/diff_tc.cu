@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tl->s_full[i], 1);
-      mbar_init(&tl->p_full[i], 129);  // + warp 3: V_j, K_{j+1} resident
+      mbar_init(&tl->p_full[i], 5);  // four warps, and warp 3: V_j, K_{j+1} resident
     }
     mbar_init(&tl->o_done, 1);
     mbar_init(&tl->g_full, 1);
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         l += u0 + u1;
       }
       tc_fence_before();
-      mbar_arrive(&tl->p_full[mp]);
+      warp_arrive(&tl->p_full[mp]);
     }
     if (ok && nkv > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(&tl->o_done, 0, abort_flag, status, WHERE_DIFF));
