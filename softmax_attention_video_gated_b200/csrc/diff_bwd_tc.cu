@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int n_stat_tiles = (a.N + 63) / 64;
   const int n = KV ? (r0 < valid ? n_stat_tiles : 0) : (valid + BS - 1) / BS;
   const float scale_log2 = scale * kLog2e;
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = warp_uniform(warp_id()), lane = lane_id();
   const int wg = warp >> 2;
 
   if (threadIdx.x == 0) {
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tl->tmem_base;
+  const uint32_t tmem = warp_uniform(tl->tmem_base);
   volatile int* abort_flag = &tl->abort_flag;
 
   if (wg == 0) {
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       constexpr uint32_t idesc_s = idesc_bf16_f32(BR, BS, false, false);      // X X'^T
       constexpr uint32_t idesc_half = idesc_bf16_f32(BR, HD / 2, false, true);  // dS_m X'_m
       constexpr uint32_t idesc_full = idesc_bf16_f32(BR, HD, false, true);      // W Y'
+      const bool leader = lane == 0;
       const uint64_t xd = smem_desc(smem_u32(smem + L::X_OFF), 16, 1024);
       const uint64_t sk = smem_desc(smem_u32(smem + L::RING), 16, 1024);      // K-major
       const uint64_t sm = smem_desc(smem_u32(smem + L::RING), BOXS, 1024);    // MN-major
@@ -174,11 +175,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint64_t bd = bb + ((m * BOXS + e * 32) >> 4);
           const uint32_t d = tmem + TM_S + 64 * m;
           if (KV)
-            umma_ss(d, xd + ((m * BOXR + e * 32) >> 4), bd, idesc_s, e != 0 ? 1u : 0u);
+            umma_ss_one(leader, d, xd + ((m * BOXR + e * 32) >> 4), bd, idesc_s, e != 0 ? 1u : 0u);
           else
-            umma_ts(d, tmem + TM_X + 8 * kk, bd, idesc_s, e != 0 ? 1u : 0u);
+            umma_ts_one(leader, d, tmem + TM_X + 8 * kk, bd, idesc_s, e != 0 ? 1u : 0u);
         }
-        umma_commit(&tl->s_full);
+        umma_commit_one(leader, &tl->s_full);
       };
       auto issue_dp = [&](int st) {
         const uint64_t bb = sk + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
@@ -186,12 +187,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint64_t bd = bb + (((kk >> 2) * BOXS + (kk & 3) * 32) >> 4);
           if (KV)
-            umma_ss(tmem + TM_DP, xd + ((2 * BOXR + (kk >> 2) * BOXR + (kk & 3) * 32) >> 4), bd,
+            umma_ss_one(leader, tmem + TM_DP, xd + ((2 * BOXR + (kk >> 2) * BOXR + (kk & 3) * 32) >> 4), bd,
                     idesc_s, kk != 0 ? 1u : 0u);
           else
-            umma_ts(tmem + TM_DP, tmem + TM_X + 64 + 8 * kk, bd, idesc_s, kk != 0 ? 1u : 0u);
+            umma_ts_one(leader, tmem + TM_DP, tmem + TM_X + 64 + 8 * kk, bd, idesc_s, kk != 0 ? 1u : 0u);
         }
-        umma_commit(&tl->dp_full);
+        umma_commit_one(leader, &tl->dp_full);
       };
       // queries stand: the last block's rows of K behind the batch's last key
       // become zero, since a weight of zero times what lies there may be NaN
@@ -218,11 +219,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = __all_sync(0xffffffffu,
                         mbar_wait(&tl->x_full, 0, abort_flag, status, WHERE_DIFF_BWD)) &&
              stage_ready(0);
-        if (ok && lane == 0) {
+        if (ok) {
           issue_s(0);
           issue_dp(0);
         }
-        __syncwarp();
       }
       for (int j = 0; j < n && ok; ++j) {
         const int st = j % STAGES, sn = (j + 1) % STAGES;
@@ -233,42 +233,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                           mbar_wait(&tl->s_empty, j & 1, abort_flag, status, WHERE_DIFF_BWD));
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) issue_s(sn);
-          __syncwarp();
+          issue_s(sn);
         }
         if (KV) {
           ok = __all_sync(0xffffffffu,
                           mbar_wait(&tl->w_full, j & 1, abort_flag, status, WHERE_DIFF_BWD));
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
-            const uint64_t yb = sm + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
+          const uint64_t yb = sm + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < BS / 16; ++kk)
-              umma_ts(tmem + TM_ACC + HD, tmem + TM_W + 32 * (j & 1) + 8 * kk,
-                      yb + (kk * 2048 >> 4), idesc_full, (kk != 0 || j != 0) ? 1u : 0u);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < BS / 16; ++kk)
+            umma_ts_one(leader, tmem + TM_ACC + HD, tmem + TM_W + 32 * (j & 1) + 8 * kk,
+                        yb + (kk * 2048 >> 4), idesc_full, (kk != 0 || j != 0) ? 1u : 0u);
         }
         ok = __all_sync(0xffffffffu,
                         mbar_wait(&tl->ds_full, j & 1, abort_flag, status, WHERE_DIFF_BWD));
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t xb = sm + static_cast<uint64_t>(st * (STAGE_BYTES >> 4));
-          // 16 columns of dS_m: those of warpgroup kk >> 1, beside its share of the other map
+        const uint64_t xb = sm + static_cast<uint64_t>(st * (STAGE_BYTES >> 4));
+        // 16 columns of dS_m: those of warpgroup kk >> 1, beside its share of the other map
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int kk = 0; kk < BS / 16; ++kk)
-              umma_ts(tmem + (KV ? TM_ACC : TM_ACCQ) + 64 * m,
-                      tmem + TM_DP + 32 * (kk >> 1) + 16 * m + 8 * (kk & 1),
-                      xb + ((m * BOXS + kk * 2048) >> 4), idesc_half,
-                      (kk != 0 || j != 0) ? 1u : 0u);
-          umma_commit(&tl->empty[st]);
-          if (more) issue_dp(sn);
-        }
-        __syncwarp();
+          for (int kk = 0; kk < BS / 16; ++kk)
+            umma_ts_one(leader, tmem + (KV ? TM_ACC : TM_ACCQ) + 64 * m,
+                        tmem + TM_DP + 32 * (kk >> 1) + 16 * m + 8 * (kk & 1),
+                        xb + ((m * BOXS + kk * 2048) >> 4), idesc_half,
+                        (kk != 0 || j != 0) ? 1u : 0u);
+        umma_commit_one(leader, &tl->empty[st]);
+        if (more) issue_dp(sn);
       }
       if (lane == 0) {
         if (ok) umma_commit(&tl->acc_done);
