@@ -13,9 +13,13 @@
 //
 // 12 warps in three warpgroups: warp 0 TMA, warp 1 TMEM and every MMA, WG1 and
 // WG2 the weights: thread r of either owns standing row r (its TMEM lane) and 32
-// of the block's 64 columns. W and dS go back to TMEM in bf16 as A operands of the
-// products; dS over dP, W beside. The next block's scores are issued as soon as
-// the threads hold this block's in registers.
+// of the block's 64 columns. The weights' loop is turned by half a step: round i
+// makes dS of block i - 1 and P (and W) of block i from dP_{i-1} and S_i, so that
+// the exponentials of one (MUFU) and the products of the other (FMA) fill the same
+// cycles, and neither waits for an MMA that needs what this round makes:
+//     MMA thread, round i:  S_i, dP_{i-1} in registers  ->  dP_i, S_{i+1}
+//                           dS_{i-1}, W_i stored        ->  dX += dS_{i-1} X', dV += W_i Y'
+// dS goes to TMEM and W to shared memory, in bf16, as A operands.
 #include <algorithm>
 
 #include "diff_common.cuh"
@@ -36,17 +40,20 @@ constexpr int TMEM_COLS = 512;
 constexpr int kRegsProducer = 56, kRegsWeights = 224;
 // TMEM columns
 constexpr int TM_S = 0;      // S_1, S_2: 64 each
-constexpr int TM_DP = 128;   // dP, then dS_1, dS_2
-constexpr int TM_W = 192;    // keys stand: W, two buffers of 32
-constexpr int TM_X = 192;    // queries stand: Q and dA as A operands, 64 each
-constexpr int TM_ACC = 256;  // keys stand: dK, dV
-constexpr int TM_ACCQ = 384; // queries stand: dQ
+constexpr int TM_DP = 128;   // dP
+constexpr int TM_DS = 192;   // dS_1, dS_2 (bf16): 16 columns of each per warpgroup
+constexpr int TM_ACC = 256;  // keys stand: dK, dV; queries stand: dQ
+constexpr int TM_X = 384;    // queries stand: Q and dA as A operands, 64 each
+constexpr int W_BYTES = BR * BS * 2;
 
 struct Tail {
   uint64_t x_full;
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
-  uint64_t s_full, s_empty, dp_full, w_full, ds_full;
+  uint64_t s_full, dp_full;  // scores in TMEM
+  uint64_t loaded;           // ... and in registers
+  uint64_t ds_full;          // dS and W stored
+  uint64_t ds_empty;         // ... and used
   uint64_t acc_done;
   uint64_t drain;
   uint32_t tmem_base;
@@ -57,7 +64,8 @@ struct Layout {
   static constexpr int X_OFF = 0;  // keys stand: K, V, two boxes each
   static constexpr int RING = KV ? 4 * BOXR : 0;
   static constexpr int STAT = RING + STAGES * STAGE_BYTES;
-  static constexpr int TAIL = STAT + (KV ? STAGES * STAT_BYTES : 0);
+  static constexpr int W_OFF = (STAT + (KV ? STAGES * STAT_BYTES : 0) + 1023) / 1024 * 1024;
+  static constexpr int TAIL = W_OFF + (KV ? W_BYTES : 0);
   static constexpr size_t SMEM = 1024 + TAIL + sizeof(Tail);
   static_assert(SMEM <= kMaxSmem, "shared memory of one CTA");
 };
@@ -95,10 +103,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&tl->empty[s], 1);
     }
     mbar_init(&tl->s_full, 1);
-    mbar_init(&tl->s_empty, kWarps);
     mbar_init(&tl->dp_full, 1);
-    mbar_init(&tl->w_full, kWarps);
+    mbar_init(&tl->loaded, kWarps);
     mbar_init(&tl->ds_full, kWarps);
+    mbar_init(&tl->ds_empty, 1);
     mbar_init(&tl->acc_done, 1);
     mbar_init(&tl->drain, 1);
     tl->abort_flag = 0;
@@ -162,10 +170,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       constexpr uint32_t idesc_s = idesc_bf16_f32(BR, BS, false, false);      // X X'^T
       constexpr uint32_t idesc_half = idesc_bf16_f32(BR, HD / 2, false, true);  // dS_m X'_m
       constexpr uint32_t idesc_full = idesc_bf16_f32(BR, HD, false, true);      // W Y'
-      const bool leader = lane == 0;
       const uint64_t xd = smem_desc(smem_u32(smem + L::X_OFF), 16, 1024);
       const uint64_t sk = smem_desc(smem_u32(smem + L::RING), 16, 1024);      // K-major
       const uint64_t sm = smem_desc(smem_u32(smem + L::RING), BOXS, 1024);    // MN-major
+      const uint64_t wd = smem_desc(smem_u32(smem + L::W_OFF), 16, 1024);
       // S_1, S_2 of the block in stage st: 64 of the 128 columns each
       auto issue_s = [&](int st) {
         const uint64_t bb = sk + static_cast<uint64_t>(st * (STAGE_BYTES >> 4));
@@ -175,11 +183,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint64_t bd = bb + ((m * BOXS + e * 32) >> 4);
           const uint32_t d = tmem + TM_S + 64 * m;
           if (KV)
-            umma_ss_one(leader, d, xd + ((m * BOXR + e * 32) >> 4), bd, idesc_s, e != 0 ? 1u : 0u);
+            umma_ss(d, xd + ((m * BOXR + e * 32) >> 4), bd, idesc_s, e != 0 ? 1u : 0u);
           else
-            umma_ts_one(leader, d, tmem + TM_X + 8 * kk, bd, idesc_s, e != 0 ? 1u : 0u);
+            umma_ts(d, tmem + TM_X + 8 * kk, bd, idesc_s, e != 0 ? 1u : 0u);
         }
-        umma_commit_one(leader, &tl->s_full);
+        umma_commit(&tl->s_full);
       };
       auto issue_dp = [&](int st) {
         const uint64_t bb = sk + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
@@ -187,12 +195,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint64_t bd = bb + (((kk >> 2) * BOXS + (kk & 3) * 32) >> 4);
           if (KV)
-            umma_ss_one(leader, tmem + TM_DP, xd + ((2 * BOXR + (kk >> 2) * BOXR + (kk & 3) * 32) >> 4), bd,
+            umma_ss(tmem + TM_DP, xd + ((2 * BOXR + (kk >> 2) * BOXR + (kk & 3) * 32) >> 4), bd,
                     idesc_s, kk != 0 ? 1u : 0u);
           else
-            umma_ts_one(leader, tmem + TM_DP, tmem + TM_X + 64 + 8 * kk, bd, idesc_s, kk != 0 ? 1u : 0u);
+            umma_ts(tmem + TM_DP, tmem + TM_X + 64 + 8 * kk, bd, idesc_s, kk != 0 ? 1u : 0u);
         }
-        umma_commit_one(leader, &tl->dp_full);
+        umma_commit(&tl->dp_full);
       };
       // queries stand: the last block's rows of K behind the batch's last key
       // become zero, since a weight of zero times what lies there may be NaN
@@ -214,56 +222,57 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         return true;
       };
+      auto wait = [&](uint64_t* bar, int parity) -> bool {
+        const bool w = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, WHERE_DIFF_BWD));
+        tc_fence_after();
+        return w;
+      };
       bool ok = true;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(&tl->x_full, 0, abort_flag, status, WHERE_DIFF_BWD)) &&
-             stage_ready(0);
-        if (ok) {
+        ok = wait(&tl->x_full, 0) && stage_ready(0);
+        if (ok && elect_one()) {
           issue_s(0);
           issue_dp(0);
         }
+        __syncwarp();
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const int st = j % STAGES, sn = (j + 1) % STAGES;
-        const bool more = j + 1 < n;
-        if (more) {
-          ok = stage_ready(j + 1) &&
-               __all_sync(0xffffffffu,
-                          mbar_wait(&tl->s_empty, j & 1, abort_flag, status, WHERE_DIFF_BWD));
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(sn);
-        }
-        if (KV) {
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&tl->w_full, j & 1, abort_flag, status, WHERE_DIFF_BWD));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t yb = sm + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < BS / 16; ++kk)
-            umma_ts_one(leader, tmem + TM_ACC + HD, tmem + TM_W + 32 * (j & 1) + 8 * kk,
-                        yb + (kk * 2048 >> 4), idesc_full, (kk != 0 || j != 0) ? 1u : 0u);
-        }
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(&tl->ds_full, j & 1, abort_flag, status, WHERE_DIFF_BWD));
+      for (int i = 0; i <= n && ok && n > 0; ++i) {
+        const int st = i % STAGES, sn = (i + 1) % STAGES, sp = (i + STAGES - 1) % STAGES;
+        ok = (i + 1 >= n || stage_ready(i + 1)) && wait(&tl->loaded, i & 1);
         if (!ok) break;
-        tc_fence_after();
-        const uint64_t xb = sm + static_cast<uint64_t>(st * (STAGE_BYTES >> 4));
-        // 16 columns of dS_m: those of warpgroup kk >> 1, beside its share of the other map
+        if (elect_one()) {
+          if (i >= 1 && i < n) issue_dp(st);
+          if (i + 1 < n) issue_s(sn);
+        }
+        __syncwarp();
+        ok = wait(&tl->ds_full, i & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          if (i >= 1) {
+            const uint64_t xb = sm + static_cast<uint64_t>(sp * (STAGE_BYTES >> 4));
+            // 16 columns of dS_m: those of warpgroup kk >> 1, beside its share of the other map
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int kk = 0; kk < BS / 16; ++kk)
-            umma_ts_one(leader, tmem + (KV ? TM_ACC : TM_ACCQ) + 64 * m,
-                        tmem + TM_DP + 32 * (kk >> 1) + 16 * m + 8 * (kk & 1),
-                        xb + ((m * BOXS + kk * 2048) >> 4), idesc_half,
-                        (kk != 0 || j != 0) ? 1u : 0u);
-        umma_commit_one(leader, &tl->empty[st]);
-        if (more) issue_dp(sn);
+              for (int kk = 0; kk < BS / 16; ++kk)
+                umma_ts(tmem + TM_ACC + 64 * m,
+                            tmem + TM_DS + 32 * (kk >> 1) + 16 * m + 8 * (kk & 1),
+                            xb + ((m * BOXS + kk * 2048) >> 4), idesc_half,
+                            (kk != 0 || i != 1) ? 1u : 0u);
+            umma_commit(&tl->empty[sp]);
+          }
+          if (KV && i < n) {
+            const uint64_t yb = sm + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < BS / 16; ++kk)
+              umma_ss(tmem + TM_ACC + HD, wd + (kk * 32 >> 4), yb + (kk * 2048 >> 4),
+                          idesc_full, (kk != 0 || i != 0) ? 1u : 0u);
+          }
+          umma_commit(&tl->ds_empty);
+        }
+        __syncwarp();
       }
-      if (lane == 0) {
+      if (elect_one()) {
         if (ok) umma_commit(&tl->acc_done);
         umma_commit(&tl->drain);
         (void)drain_wait(&tl->drain, 0);
@@ -310,96 +319,105 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       nl = f2pack(f[4], f[4]);
     }
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const float* stat = reinterpret_cast<const float*>(smem + L::STAT + (j % STAGES) * STAT_BYTES) +
-                          32 * half;
-      // the stage's statistics landed before the scores were made of its rows, but this
-      // thread has to see that copy itself
-      bool w = !KV || mbar_wait(&tl->full[j % STAGES], (j / STAGES) & 1, abort_flag, status,
-                                WHERE_DIFF_BWD);
-      w = w && mbar_wait(&tl->s_full, j & 1, abort_flag, status, WHERE_DIFF_BWD);
+    uint64_t p1[16], q2[16];  // P_1 and -lambda P_2 of a block
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p1[i] = q2[i] = 0;
+    const float* stat0 = reinterpret_cast<const float*>(smem + L::STAT) + 32 * half;
+    for (int i = 0; i <= n && n > 0; ++i) {
+      const float* stat = stat0 + (i % STAGES) * (STAT_BYTES / 4);                   // block i's
+      const float* prev = stat0 + ((i + STAGES - 1) % STAGES) * (STAT_BYTES / 4);  // block i - 1's
+      bool w = true;
+      if (i < n) {
+        // the stage's statistics landed before the scores were made of its rows, but
+        // this thread has to see that copy itself
+        if (KV) w = mbar_wait(&tl->full[i % STAGES], (i / STAGES) & 1, abort_flag, status, WHERE_DIFF_BWD);
+        w = w && mbar_wait(&tl->s_full, i & 1, abort_flag, status, WHERE_DIFF_BWD);
+      }
+      if (i > 0) w = w && mbar_wait(&tl->dp_full, (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
       if (!__all_sync(0xffffffffu, w)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t s1[32], s2[32];
+      uint32_t s1[32], s2[32], dp[32];
+      // in the last round the scores are the round's before; nothing made of them is used
       tmem_ld32(lane_base + TM_S + 32 * half, s1);
       tmem_ld32(lane_base + TM_S + 64 + 32 * half, s2);
+      if (i > 0) {
+        tmem_ld32(lane_base + TM_DP + 32 * half, dp);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) dp[k] = 0u;
+      }
       tmem_wait_ld();
       tc_fence_before();
-      warp_arrive(&tl->s_empty);
-      uint64_t p1[16], q2[16];  // P_1 and -lambda P_2
-      uint32_t wk[16];
-      ulonglong2 f1, f2, f3;  // two pairs of queries' statistics at a time
+      warp_arrive(&tl->loaded);
+      uint32_t d1[16], d2[16], wk[16];
+      ulonglong2 f1, f2, f3, g1, g2;  // two pairs of queries' statistics at a time
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int k = 0; k < 16; ++k) {
         if (KV) {
-          if (i % 2 == 0) {
-            f1 = *reinterpret_cast<const ulonglong2*>(stat + 2 * i);
-            f2 = *reinterpret_cast<const ulonglong2*>(stat + 64 + 2 * i);
-            f3 = *reinterpret_cast<const ulonglong2*>(stat + 256 + 2 * i);
+          if (k % 2 == 0) {
+            g1 = *reinterpret_cast<const ulonglong2*>(prev + 128 + 2 * k);
+            g2 = *reinterpret_cast<const ulonglong2*>(prev + 192 + 2 * k);
+            f1 = *reinterpret_cast<const ulonglong2*>(stat + 2 * k);
+            f2 = *reinterpret_cast<const ulonglong2*>(stat + 64 + 2 * k);
+            f3 = *reinterpret_cast<const ulonglong2*>(stat + 256 + 2 * k);
           }
-          nlse1 = i % 2 == 0 ? f1.x : f1.y;
-          nlse2 = i % 2 == 0 ? f2.x : f2.y;
-          nl = i % 2 == 0 ? f3.x : f3.y;
+          nd1 = k % 2 == 0 ? g1.x : g1.y;
+          nd2 = k % 2 == 0 ? g2.x : g2.y;
+          nlse1 = k % 2 == 0 ? f1.x : f1.y;
+          nlse2 = k % 2 == 0 ? f2.x : f2.y;
+          nl = k % 2 == 0 ? f3.x : f3.y;
         }
         float x0, x1, y0, y1;
-        f2unpack(fma_f2(f2pack(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])), scale2,
+        const uint64_t dpp = f2pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1]));
+        f2unpack(mul_f2(p1[k], add_f2(dpp, nd1)), x0, x1);
+        f2unpack(mul_f2(q2[k], add_f2(dpp, nd2)), y0, y1);
+        d1[k] = pack_bf16x2(x0, x1);
+        d2[k] = pack_bf16x2(y0, y1);
+        f2unpack(fma_f2(f2pack(__uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1])), scale2,
                         nlse1), x0, x1);
-        f2unpack(fma_f2(f2pack(__uint_as_float(s2[2 * i]), __uint_as_float(s2[2 * i + 1])), scale2,
+        f2unpack(fma_f2(f2pack(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])), scale2,
                         nlse2), y0, y1);
-        p1[i] = f2pack(ex2_mufu(x0), ex2_mufu(x1));
-        q2[i] = mul_f2(f2pack(ex2_mufu(y0), ex2_mufu(y1)), nl);
+        p1[k] = f2pack(ex2_mufu(x0), ex2_mufu(x1));
+        q2[k] = mul_f2(f2pack(ex2_mufu(y0), ex2_mufu(y1)), nl);
         if (KV) {
-          float w0, w1;
-          f2unpack(add_f2(p1[i], q2[i]), w0, w1);
-          wk[i] = pack_bf16x2(w0, w1);
+          f2unpack(add_f2(p1[k], q2[k]), x0, x1);
+          wk[k] = pack_bf16x2(x0, x1);
         }
       }
-      if (KV) {
-        tmem_st16(lane_base + TM_W + 32 * (j & 1) + 16 * half, wk);
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(&tl->w_full);
+      if (!KV) {  // keys of block i - 1 that count; of block 0's, none behind
+        const int left = valid - (i - 1) * BS - 32 * half;
+        if (left < 32) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t keep = (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
+            d1[k] &= keep;
+            d2[k] &= keep;
+          }
+        }
       }
-      w = mbar_wait(&tl->dp_full, j & 1, abort_flag, status, WHERE_DIFF_BWD);
+      // the products of the round before have used dS and W
+      w = i == 0 || mbar_wait(&tl->ds_empty, (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
       if (!__all_sync(0xffffffffu, w)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t dp[32], d1[16], d2[16];
-      tmem_ld32(lane_base + TM_DP + 32 * half, dp);
-      tmem_wait_ld();
-      const int left = valid - j * BS - 32 * half;  // queries stand: keys that count
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (KV) {
-          if (i % 2 == 0) {
-            f1 = *reinterpret_cast<const ulonglong2*>(stat + 128 + 2 * i);
-            f2 = *reinterpret_cast<const ulonglong2*>(stat + 192 + 2 * i);
-          }
-          nd1 = i % 2 == 0 ? f1.x : f1.y;
-          nd2 = i % 2 == 0 ? f2.x : f2.y;
-        }
-        const uint64_t dpp = f2pack(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
-        float x0, x1, y0, y1;
-        f2unpack(mul_f2(p1[i], add_f2(dpp, nd1)), x0, x1);
-        f2unpack(mul_f2(q2[i], add_f2(dpp, nd2)), y0, y1);
-        d1[i] = pack_bf16x2(x0, x1);
-        d2[i] = pack_bf16x2(y0, y1);
+      if (i > 0) {
+        tmem_st16(lane_base + TM_DS + 32 * half, d1);
+        tmem_st16(lane_base + TM_DS + 32 * half + 16, d2);
       }
-      if (!KV && left < 32) {
+      if (KV && i < n) {
+        // row r of W, 128-byte swizzle: chunk c of the row at c ^ (r & 7)
+        uint8_t* wrow = smem + L::W_OFF + r * 128;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t keep = (2 * i < left ? 0xFFFFu : 0u) | (2 * i + 1 < left ? 0xFFFF0000u : 0u);
-          d1[i] &= keep;
-          d2[i] &= keep;
-        }
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(wrow + (((4 * half + c) ^ (r & 7)) << 4)) =
+              make_uint4(wk[4 * c], wk[4 * c + 1], wk[4 * c + 2], wk[4 * c + 3]);
+        fence_proxy_async_smem();
       }
-      tmem_st16(lane_base + TM_DP + 32 * half, d1);
-      tmem_st16(lane_base + TM_DP + 32 * half + 16, d2);
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&tl->ds_full);
@@ -420,7 +438,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       f = half == 0 ? scale : 1.0f;
     } else {
       dst = static_cast<__nv_bfloat16*>(g.dq) + at * g.lddq + 64 * half;
-      col0 = TM_ACCQ + 64 * half;
+      col0 = TM_ACC + 64 * half;
       ncols = 64;
       f = scale;
     }

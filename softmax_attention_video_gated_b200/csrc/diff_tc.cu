@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     kb0 = u.part * nkv / wk.split;
     nkv = (u.part + 1) * nkv / wk.split - kb0;
   }
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = warp_uniform(warp_id()), lane = lane_id();
   const int wg = warp >> 2;
 
   if (threadIdx.x == 0) {
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tl->tmem_base;
+  const uint32_t tmem = warp_uniform(tl->tmem_base);
   volatile int* abort_flag = &tl->abort_flag;
 
   if (wg == 0) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         mbar_wait(&tl->k_full[0], 0, abort_flag, status, WHERE_DIFF));
         if (ok) {
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             issue_s(0, 0);
             issue_s(1, 0);
             umma_commit(&tl->k_empty[0]);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             issue_pv(m, vst, j == 0);
             if (m == 1) umma_commit(&tl->v_empty[vst]);
             if (more) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         vst = vst + 1 == V_STAGES ? 0 : vst + 1;
         kn = kn + 1 == K_STAGES ? 0 : kn + 1;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         if (ok) umma_commit(&tl->o_done);
         umma_commit(&tl->drain);
         (void)drain_wait(&tl->drain, 0);
