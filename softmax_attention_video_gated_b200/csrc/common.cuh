@@ -357,6 +357,55 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
+// The same MMAs with descriptors as base and constant offset: `a` and `b` are the
+// lower words of descriptors whose upper words are desc_hi(), `AOFF` and `BOFF`
+// bytes are added to their addresses. Only the few bases stay in registers.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo_bytes) {
+  return (sbo_bytes >> 4) | (1u << 14) | (2u << 29);
+}
+template <int AOFF, int BOFF>
+__device__ __forceinline__ void umma_ss_at(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
+      "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(AOFF >> 4), "n"(BOFF >> 4),
+      "n"(static_cast<int>(desc_hi(1024)))
+      : "memory");
+}
+template <int BOFF>
+__device__ __forceinline__ void umma_ts_at(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 y, %2, %5;\n\t"
+      "mov.b64 db, {y, %6};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(BOFF >> 4),
+      "n"(static_cast<int>(desc_hi(1024)))
+      : "memory");
+}
+// lower word of a descriptor: start address and leading byte offset
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo_bytes >> 4) & 0x3FFFu) << 16);
+}
+// f(constant 0), ..., f(constant n - 1)
+template <int I>
+struct Int {
+  static constexpr int value = I;
+};
+template <int N, typename F, int I = 0>
+__device__ __forceinline__ void unrolled(const F& f) {
+  if constexpr (I < N) {
+    f(Int<I>());
+    unrolled<N, F, I + 1>(f);
+  }
+}
+
 // a value that all lanes hold alike, in a form that the compiler can tell
 __device__ __forceinline__ int warp_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -389,6 +438,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {

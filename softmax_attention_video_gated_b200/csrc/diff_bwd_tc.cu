@@ -11,14 +11,15 @@
 // Either recomputes the scores: 7/5 of the products of one pass over the pairs,
 // against adding dQ into memory in an order that changes from run to run.
 //
-// 12 warps in three warpgroups: warp 0 TMA, warp 1 TMEM and every MMA, WG1 and
-// WG2 the weights: thread r of either owns standing row r (its TMEM lane) and 32
+// 12 warps in three warpgroups: warp 0 TMA, warp 1 TMEM and the scores' MMAs, warp 3
+// the products' MMAs, WG1 and WG2 the weights: thread r of either owns standing row r (its TMEM lane) and 32
 // of the block's 64 columns. The weights' loop is turned by half a step: round i
 // makes dS of block i - 1 and P (and W) of block i from dP_{i-1} and S_i, so that
 // the exponentials of one (MUFU) and the products of the other (FMA) fill the same
 // cycles, and neither waits for an MMA that needs what this round makes:
-//     MMA thread, round i:  S_i, dP_{i-1} in registers  ->  dP_i, S_{i+1}
-//                           dS_{i-1}, W_i stored        ->  dX += dS_{i-1} X', dV += W_i Y'
+//     warp 1, round i:  S_i, dP_{i-1} in registers  ->  dP_i, S_{i+1}
+//     warp 3, round i:  dS_{i-1}, W_i stored        ->  dX += dS_{i-1} X', dV += W_i Y'
+// What one warp's MMAs need of the other's goes through the weights' barriers.
 // dS goes to TMEM and W to shared memory, in bf16, as A operands.
 #include <algorithm>
 
@@ -52,10 +53,10 @@ struct Tail {
   uint64_t empty[STAGES];
   uint64_t s_full, dp_full;  // scores in TMEM
   uint64_t loaded;           // ... and in registers
-  uint64_t ds_full;          // dS and W stored
-  uint64_t ds_empty;         // ... and used
+  uint64_t ds_full[2];       // a warpgroup's dS and W stored
+  uint64_t ds_empty[2];      // ... and used
   uint64_t acc_done;
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -69,6 +70,12 @@ struct Layout {
   static constexpr size_t SMEM = 1024 + TAIL + sizeof(Tail);
   static_assert(SMEM <= kMaxSmem, "shared memory of one CTA");
 };
+
+// a whole warp's wait
+__device__ __forceinline__ bool mma_wait(uint64_t* bar, int parity, volatile int* abort_flag,
+                                         int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, WHERE_DIFF_BWD));
+}
 
 template <bool KV>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -105,10 +112,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(&tl->s_full, 1);
     mbar_init(&tl->dp_full, 1);
     mbar_init(&tl->loaded, kWarps);
-    mbar_init(&tl->ds_full, kWarps);
-    mbar_init(&tl->ds_empty, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&tl->ds_full[w], kWarps / 2);
+      mbar_init(&tl->ds_empty[w], 1);
+    }
     mbar_init(&tl->acc_done, 1);
-    mbar_init(&tl->drain, 1);
+    mbar_init(&tl->drain[0], 1);
+    mbar_init(&tl->drain[1], 1);
     tl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -166,46 +176,39 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // ------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc_s = idesc_bf16_f32(BR, BS, false, false);      // X X'^T
-      constexpr uint32_t idesc_half = idesc_bf16_f32(BR, HD / 2, false, true);  // dS_m X'_m
-      constexpr uint32_t idesc_full = idesc_bf16_f32(BR, HD, false, true);      // W Y'
-      const uint64_t xd = smem_desc(smem_u32(smem + L::X_OFF), 16, 1024);
-      const uint64_t sk = smem_desc(smem_u32(smem + L::RING), 16, 1024);      // K-major
-      const uint64_t sm = smem_desc(smem_u32(smem + L::RING), BOXS, 1024);    // MN-major
-      const uint64_t wd = smem_desc(smem_u32(smem + L::W_OFF), 16, 1024);
+      // ------------------------------------------------ MMAs: scores
+      constexpr uint32_t idesc_s = idesc_bf16_f32(BR, BS, false, false);  // X X'^T
+      const uint32_t xd = warp_uniform(desc_lo(smem_u32(smem + L::X_OFF), 16));
+      const uint32_t sk = warp_uniform(desc_lo(smem_u32(smem + L::RING), 16));
       // S_1, S_2 of the block in stage st: 64 of the 128 columns each
       auto issue_s = [&](int st) {
-        const uint64_t bb = sk + static_cast<uint64_t>(st * (STAGE_BYTES >> 4));
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const int m = kk >> 2, e = kk & 3;
-          const uint64_t bd = bb + ((m * BOXS + e * 32) >> 4);
+        const uint32_t bb = sk + static_cast<uint32_t>(st * (STAGE_BYTES >> 4));
+        unrolled<HD / 16>([&](auto k) {
+          constexpr int kk = decltype(k)::value, m = kk >> 2, e = kk & 3;
           const uint32_t d = tmem + TM_S + 64 * m;
           if (KV)
-            umma_ss(d, xd + ((m * BOXR + e * 32) >> 4), bd, idesc_s, e != 0 ? 1u : 0u);
+            umma_ss_at<m * BOXR + e * 32, m * BOXS + e * 32>(d, xd, bb, idesc_s, e != 0 ? 1u : 0u);
           else
-            umma_ts(d, tmem + TM_X + 8 * kk, bd, idesc_s, e != 0 ? 1u : 0u);
-        }
+            umma_ts_at<m * BOXS + e * 32>(d, tmem + TM_X + 8 * kk, bb, idesc_s, e != 0 ? 1u : 0u);
+        });
         umma_commit(&tl->s_full);
       };
       auto issue_dp = [&](int st) {
-        const uint64_t bb = sk + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint64_t bd = bb + (((kk >> 2) * BOXS + (kk & 3) * 32) >> 4);
+        const uint32_t bb = sk + static_cast<uint32_t>(st * (STAGE_BYTES >> 4));
+        unrolled<HD / 16>([&](auto k) {
+          constexpr int kk = decltype(k)::value, m = kk >> 2, e = kk & 3;
           if (KV)
-            umma_ss(tmem + TM_DP, xd + ((2 * BOXR + (kk >> 2) * BOXR + (kk & 3) * 32) >> 4), bd,
-                    idesc_s, kk != 0 ? 1u : 0u);
+            umma_ss_at<(2 + m) * BOXR + e * 32, (2 + m) * BOXS + e * 32>(tmem + TM_DP, xd, bb, idesc_s,
+                                                                         kk != 0 ? 1u : 0u);
           else
-            umma_ts(tmem + TM_DP, tmem + TM_X + 64 + 8 * kk, bd, idesc_s, kk != 0 ? 1u : 0u);
-        }
+            umma_ts_at<(2 + m) * BOXS + e * 32>(tmem + TM_DP, tmem + TM_X + 64 + 8 * kk, bb, idesc_s,
+                                                kk != 0 ? 1u : 0u);
+        });
         umma_commit(&tl->dp_full);
       };
       // queries stand: the last block's rows of K behind the batch's last key
       // become zero, since a weight of zero times what lies there may be NaN
-      auto stage_ready = [&](int j) -> bool {
-        const int st = j % STAGES;
+      auto stage_ready = [&](int j, int st) -> bool {
         if (!__all_sync(0xffffffffu, mbar_wait(&tl->full[st], (j / STAGES) & 1, abort_flag, status,
                                                WHERE_DIFF_BWD)))
           return false;
@@ -219,63 +222,88 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        tc_fence_after();
         return true;
       };
-      auto wait = [&](uint64_t* bar, int parity) -> bool {
-        const bool w = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, WHERE_DIFF_BWD));
+      bool ok = n > 0 && mma_wait(&tl->x_full, 0, abort_flag, status) && stage_ready(0, 0);
+      if (ok) {
         tc_fence_after();
-        return w;
-      };
-      bool ok = true;
-      if (n > 0) {
-        ok = wait(&tl->x_full, 0) && stage_ready(0);
-        if (ok && elect_one()) {
+        if (elect_one()) {
           issue_s(0);
           issue_dp(0);
         }
         __syncwarp();
       }
-      for (int i = 0; i <= n && ok && n > 0; ++i) {
-        const int st = i % STAGES, sn = (i + 1) % STAGES, sp = (i + STAGES - 1) % STAGES;
-        ok = (i + 1 >= n || stage_ready(i + 1)) && wait(&tl->loaded, i & 1);
+      int st = 0;  // stage of block i
+      for (int i = 0; i < n && ok; ++i) {
+        const bool more = i + 1 < n;
+        const int sn = st + 1 == STAGES ? 0 : st + 1;
+        ok = (!more || stage_ready(i + 1, sn)) && mma_wait(&tl->loaded, i & 1, abort_flag, status);
         if (!ok) break;
+        tc_fence_after();
         if (elect_one()) {
-          if (i >= 1 && i < n) issue_dp(st);
-          if (i + 1 < n) issue_s(sn);
+          if (i >= 1) issue_dp(st);
+          if (more) issue_s(sn);
         }
         __syncwarp();
-        ok = wait(&tl->ds_full, i & 1);
-        if (!ok) break;
-        if (elect_one()) {
-          if (i >= 1) {
-            const uint64_t xb = sm + static_cast<uint64_t>(sp * (STAGE_BYTES >> 4));
-            // 16 columns of dS_m: those of warpgroup kk >> 1, beside its share of the other map
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int kk = 0; kk < BS / 16; ++kk)
-                umma_ts(tmem + TM_ACC + 64 * m,
-                            tmem + TM_DS + 32 * (kk >> 1) + 16 * m + 8 * (kk & 1),
-                            xb + ((m * BOXS + kk * 2048) >> 4), idesc_half,
-                            (kk != 0 || i != 1) ? 1u : 0u);
-            umma_commit(&tl->empty[sp]);
-          }
-          if (KV && i < n) {
-            const uint64_t yb = sm + static_cast<uint64_t>((st * STAGE_BYTES + 2 * BOXS) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < BS / 16; ++kk)
-              umma_ss(tmem + TM_ACC + HD, wd + (kk * 32 >> 4), yb + (kk * 2048 >> 4),
-                          idesc_full, (kk != 0 || i != 0) ? 1u : 0u);
-          }
-          umma_commit(&tl->ds_empty);
+        st = sn;
+      }
+      if (elect_one()) {
+        umma_commit(&tl->drain[0]);
+        (void)drain_wait(&tl->drain[0], 0);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ------------------------------------------------ MMAs: products
+      constexpr uint32_t idesc_half = idesc_bf16_f32(BR, HD / 2, false, true);  // dS_m X'_m
+      constexpr uint32_t idesc_full = idesc_bf16_f32(BR, HD, false, true);      // W Y'
+      const uint32_t sm = warp_uniform(desc_lo(smem_u32(smem + L::RING), BOXS));
+      const uint32_t wd = warp_uniform(desc_lo(smem_u32(smem + L::W_OFF), 16));
+      // warpgroup w's half of round i: dX += dS_{i-1} X', dV += W_i Y'; st, sp: the
+      // stages of blocks i and i - 1
+      auto products = [&](auto wc, int i, int st, int sp) {
+        constexpr int w = decltype(wc)::value;
+        if (i >= 1) {
+          const uint32_t xb = sm + static_cast<uint32_t>(sp * (STAGE_BYTES >> 4));
+          const uint32_t first = w != 0 || i != 1 ? 1u : 0u;
+          unrolled<BS / 16>([&](auto k) {
+            constexpr int m = decltype(k)::value >> 1, kk = decltype(k)::value & 1;
+            umma_ts_at<m * BOXS + (2 * w + kk) * 2048>(tmem + TM_ACC + 64 * m,
+                                                       tmem + TM_DS + 32 * w + 16 * m + 8 * kk, xb,
+                                                       idesc_half, kk != 0 ? 1u : first);
+          });
+          if (w == 1) umma_commit(&tl->empty[sp]);  // the stage's last use
         }
+        if (KV && i < n) {
+          const uint32_t yb = sm + static_cast<uint32_t>(st * (STAGE_BYTES >> 4));
+          const uint32_t first = w != 0 || i != 0 ? 1u : 0u;
+          unrolled<BS / 32>([&](auto k) {
+            constexpr int kk = decltype(k)::value;
+            umma_ss_at<(2 * w + kk) * 32, 2 * BOXS + (2 * w + kk) * 2048>(
+                tmem + TM_ACC + HD, wd, yb, idesc_full, kk != 0 ? 1u : first);
+          });
+        }
+        umma_commit(&tl->ds_empty[w]);
+      };
+      bool ok = n > 0;
+      int st = 0, sp = STAGES - 1;
+      for (int i = 0; i <= n && ok; ++i) {
+        ok = mma_wait(&tl->ds_full[0], i & 1, abort_flag, status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) products(Int<0>(), i, st, sp);
         __syncwarp();
+        ok = mma_wait(&tl->ds_full[1], i & 1, abort_flag, status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) products(Int<1>(), i, st, sp);
+        __syncwarp();
+        sp = st;
+        st = st + 1 == STAGES ? 0 : st + 1;
       }
       if (elect_one()) {
         if (ok) umma_commit(&tl->acc_done);
-        umma_commit(&tl->drain);
-        (void)drain_wait(&tl->drain, 0);
+        umma_commit(&tl->drain[1]);
+        (void)drain_wait(&tl->drain[1], 0);
       }
       __syncwarp();
     }
@@ -399,7 +427,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       // the products of the round before have used dS and W
-      w = i == 0 || mbar_wait(&tl->ds_empty, (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
+      w = i == 0 || mbar_wait(&tl->ds_empty[half], (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
       if (!__all_sync(0xffffffffu, w)) {
         ok = false;
         break;
@@ -420,7 +448,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(&tl->ds_full);
+      warp_arrive(&tl->ds_full[half]);
     }
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(&tl->acc_done, 0, abort_flag, status, WHERE_DIFF_BWD));
