@@ -20,7 +20,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsva.so")
 SOURCES = ["sva_abi.cu", "gemm_tc.cu", "linear_tc.cu", "anchor_tc.cu", "aux_kernels.cu",
            "f32_kernels.cu", "noalloc.cu", "diff_f32.cu", "diff_aux.cu",
-           "diff_tc.cu", "diff_bwd_tc.cu", "block_norm.cu"]
+           "diff_tc.cu", "diff_few.cu", "diff_bwd_tc.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]

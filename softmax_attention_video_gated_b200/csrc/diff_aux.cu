@@ -160,6 +160,7 @@ cudaError_t prepare(const sva_diff_args& a, const sva_diff_grads& g, const DiffB
 
 DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt) {
   DiffPlan p;
+  if (N <= kDiffFewRows) return p;  // no tiles, no scratch
   const bool tc = dt == SVA_BF16;
   p.rows = tc ? kDiffTcRows : kDiffF32Rows;
   const int keys = tc ? kDiffTcKeys : kDiffF32Keys;

@@ -142,6 +142,10 @@ struct DiffPlan {
   size_t partial_bytes = 0;
   unsigned grid() const { return static_cast<unsigned>(n_full + n_split_units * split); }
 };
+// at most this many queries a batch go to the kernel that reads K and V once
+constexpr int kDiffFewRows = 4;
+// (it waits for nothing, reports nothing and writes the status words itself)
+cudaError_t diff_fwd_few(const sva_diff_args& a, int* status, cudaStream_t s);
 DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt);
 cudaError_t diff_fwd_f32(const sva_diff_args& a, void* scratch, cudaStream_t s);
 cudaError_t diff_fwd_bf16(const sva_diff_args& a, int* status, void* scratch, cudaStream_t s);

@@ -301,11 +301,15 @@ extern "C" sva_status_t sva_diff_anchor_fwd(const sva_diff_args* args, void* ws,
                                                  args->dtype))
     return SVA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = clear_status(ws, s)) != SVA_OK) return st;
   void* scratch = static_cast<char*>(ws) + SVA_STATUS_BYTES;
-  const cudaError_t e = args->dtype == SVA_BF16
-                            ? diff_fwd_bf16(*args, static_cast<int*>(ws), scratch, s)
-                            : diff_fwd_f32(*args, scratch, s);
+  cudaError_t e;
+  if (args->N <= kDiffFewRows) {
+    e = diff_fwd_few(*args, static_cast<int*>(ws), s);
+  } else {
+    if ((st = clear_status(ws, s)) != SVA_OK) return st;
+    e = args->dtype == SVA_BF16 ? diff_fwd_bf16(*args, static_cast<int*>(ws), scratch, s)
+                                : diff_fwd_f32(*args, scratch, s);
+  }
   return e == cudaSuccess ? SVA_OK : cuda_fail(e);
 }
 

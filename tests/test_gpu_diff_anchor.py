@@ -125,6 +125,7 @@ SHAPES = [
     (2, 1, 300, 2),        # one query against many keys
     (1, 1, 20000, 1),      # ... split over many CTAs
     (1, 300, 1, 2),        # one key
+    (2, 2, 700, 2), (1, 4, 5000, 3), (1, 3, 33, 1), (3, 1, 4095, 1),  # a handful, cut over clusters
     (1, 64, 64, 1), (1, 128, 128, 2), (1, 65, 129, 3), (2, 127, 63, 2), (1, 256, 192, 1),
     (2, 257, 1000, 1), (3, 333, 333, 2), (1, 5, 4097, 2),
 ]
@@ -158,6 +159,19 @@ def test_padded_batch(dtype, lens):
         t["v"][b, max(n, 0):] = float("inf")
     ref = compare(x, t, 2, dtype, lens=lens)
     assert np.all(ref["dk"][0, max(lens[0], 0):] == 0)
+
+
+@pytest.mark.parametrize("dtype, d", [("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("N", [1, 2, 4])
+@pytest.mark.parametrize("lens", [[3000, 0, 1], [17, 2049, 2999], [-1, 9999, 8]])
+def test_padded_batch_of_a_few_queries(dtype, d, N, lens):
+    # key counts that leave some or all CTAs of a cluster without keys
+    x = make(3, N, 3000, 2, d, dtype, 15)
+    t = dev(x, dtype)
+    for b, n in enumerate(lens):
+        t["k"][b, max(n, 0):] = float("nan")
+        t["v"][b, max(n, 0):] = float("inf")
+    compare(x, t, 2, dtype, lens=lens)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
