@@ -29,33 +29,47 @@ __device__ __forceinline__ void load_rows(float* dst, const void* src, int64_t l
   }
 }
 
-// acc[i][j] += sum_k a[ty*RI + i][k0 + k] b[tx + 16 j][k0 + k], k < K (row strides LA, LB)
+// acc[i][j] = sum_k a[ty*RI + i][k] b[tx + 16 j][k], k < K (row strides LA, LB).
+// The even and the odd k are summed apart, so that a packed fp32 pair takes both.
 template <int RI, int RJ, int K, int LA, int LB>
 __device__ __forceinline__ void dot_tile(const float* a, const float* b, int tx, int ty,
                                          float (&acc)[RI][RJ]) {
+  uint64_t p[RI][RJ];
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) p[i][j] = 0;
 #pragma unroll 4
   for (int k = 0; k < K; k += 4) {
-    float4 av[RI], bv[RJ];
+    ulonglong2 av[RI], bv[RJ];
 #pragma unroll
-    for (int i = 0; i < RI; ++i) av[i] = *reinterpret_cast<const float4*>(a + (ty * RI + i) * LA + k);
+    for (int i = 0; i < RI; ++i)
+      av[i] = *reinterpret_cast<const ulonglong2*>(a + (ty * RI + i) * LA + k);
 #pragma unroll
-    for (int j = 0; j < RJ; ++j) bv[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * LB + k);
+    for (int j = 0; j < RJ; ++j)
+      bv[j] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * j) * LB + k);
 #pragma unroll
     for (int i = 0; i < RI; ++i)
 #pragma unroll
       for (int j = 0; j < RJ; ++j) {
-        acc[i][j] = fmaf(av[i].x, bv[j].x, acc[i][j]);
-        acc[i][j] = fmaf(av[i].y, bv[j].y, acc[i][j]);
-        acc[i][j] = fmaf(av[i].z, bv[j].z, acc[i][j]);
-        acc[i][j] = fmaf(av[i].w, bv[j].w, acc[i][j]);
+        p[i][j] = fma_f2(av[i].x, bv[j].x, p[i][j]);
+        p[i][j] = fma_f2(av[i].y, bv[j].y, p[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) {
+      float lo, hi;
+      f2unpack(p[i][j], lo, hi);
+      acc[i][j] = lo + hi;
+    }
 }
 
-// acc[i][4 j + e] += sum_k p[ty*RI + i][k] x[k][c0 + 64 j + 4 tx + e], k < K
+// acc[i][2 j + e] += sum_k p[ty*RI + i][k] x[k][64 j + 4 tx + 2 e, + 1], k < K: pairs of columns
 template <int RI, int RJ, int K, int LP, int LX>
 __device__ __forceinline__ void mix_tile(const float* p, const float* x, int tx, int ty,
-                                         float (&acc)[RI][4 * RJ]) {
+                                         uint64_t (&acc)[RI][2 * RJ]) {
 #pragma unroll 2
   for (int k = 0; k < K; k += 4) {
     float4 pv[RI];
@@ -65,18 +79,23 @@ __device__ __forceinline__ void mix_tile(const float* p, const float* x, int tx,
     for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
       for (int j = 0; j < RJ; ++j) {
-        const float4 xv = *reinterpret_cast<const float4*>(x + (k + kk) * LX + 64 * j + 4 * tx);
+        const ulonglong2 xv = *reinterpret_cast<const ulonglong2*>(x + (k + kk) * LX + 64 * j + 4 * tx);
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
           const float w = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
-          acc[i][4 * j] = fmaf(w, xv.x, acc[i][4 * j]);
-          acc[i][4 * j + 1] = fmaf(w, xv.y, acc[i][4 * j + 1]);
-          acc[i][4 * j + 2] = fmaf(w, xv.z, acc[i][4 * j + 2]);
-          acc[i][4 * j + 3] = fmaf(w, xv.w, acc[i][4 * j + 3]);
+          const uint64_t w2 = f2pack(w, w);
+          acc[i][2 * j] = fma_f2(w2, xv.x, acc[i][2 * j]);
+          acc[i][2 * j + 1] = fma_f2(w2, xv.y, acc[i][2 * j + 1]);
         }
       }
     }
   }
+}
+__device__ __forceinline__ float4 quad(uint64_t a, uint64_t b) {
+  float4 v;
+  f2unpack(a, v.x, v.y);
+  f2unpack(b, v.z, v.w);
+  return v;
 }
 
 __device__ __forceinline__ float row_max16(float v) {
@@ -94,7 +113,7 @@ __device__ __forceinline__ float row_sum16(float v) {
 // forward
 // ---------------------------------------------------------------------------
 
-// query rows and keys of a tile: 128 threads, 4 x 2 scores each
+// query rows and keys of a tile: 128 threads, 4 x 4 scores of a map each
 constexpr int FR = kDiffF32Rows, FK = kDiffF32Keys;
 
 template <int D>
@@ -121,7 +140,7 @@ __global__ void __launch_bounds__(128) diff_fwd_kernel(const sva_diff_args a, fl
   const int kb1 = u.part < 0 ? nkb : (u.part + 1) * nkb / wk.split;
   const int q0 = u.q0;
   load_rows<FR, D>(qs, a.q, a.ldq, b, a.N, h * D, q0, a.N);
-  float o[2][4][4 * RJ] = {};
+  uint64_t o[2][4][2 * RJ] = {};
   float m[2][4], l[2][4];
 #pragma unroll
   for (int mm = 0; mm < 2; ++mm)
@@ -134,24 +153,31 @@ __global__ void __launch_bounds__(128) diff_fwd_kernel(const sva_diff_args a, fl
     __syncthreads();
 #pragma unroll
     for (int mm = 0; mm < 2; ++mm) {
-      float s[4][2] = {};
-      dot_tile<4, 2, M, L, L>(qs + mm * M, ks + mm * M, tx, ty, s);
+      float s[4][FK / 16];
+      dot_tile<4, FK / 16, M, L, L>(qs + mm * M, ks + mm * M, tx, ty, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < FK / 16; ++j) {
           s[i][j] = kb * FK + tx + 16 * j < valid ? s[i][j] * scale_log2 : -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
         // a block holds one valid key at least, so the new maximum is finite
-        const float mx = fmaxf(m[mm][i], row_max16(fmaxf(s[i][0], s[i][1])));
+        const float mx = fmaxf(m[mm][i], row_max16(top));
         const float f = exp2f(m[mm][i] - mx);
         m[mm][i] = mx;
-        const float p0 = exp2f(s[i][0] - mx), p1 = exp2f(s[i][1] - mx);
-        l[mm][i] = fmaf(l[mm][i], f, row_sum16(p0 + p1));
-#pragma unroll
-        for (int e = 0; e < 4 * RJ; ++e) o[mm][i][e] *= f;
         float* pr = ps + (mm * FR + ty * 4 + i) * LP;
-        pr[tx] = p0;
-        pr[tx + 16] = p1;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < FK / 16; ++j) {
+          const float p = exp2f(s[i][j] - mx);
+          pr[tx + 16 * j] = p;
+          sum += p;
+        }
+        l[mm][i] = fmaf(l[mm][i], f, row_sum16(sum));
+#pragma unroll
+        for (int e = 0; e < 2 * RJ; ++e) o[mm][i][e] = mul_f2(o[mm][i][e], f2pack(f, f));
       }
     }
     // a row of P is written and read by the same half warp
@@ -171,7 +197,7 @@ __global__ void __launch_bounds__(128) diff_fwd_kernel(const sva_diff_args a, fl
 #pragma unroll
         for (int j = 0; j < RJ; ++j)
           *reinterpret_cast<float4*>(po + r * D + 64 * j + 4 * tx) =
-              make_float4(o[mm][i][4 * j], o[mm][i][4 * j + 1], o[mm][i][4 * j + 2], o[mm][i][4 * j + 3]);
+              quad(o[mm][i][2 * j], o[mm][i][2 * j + 1]);
         if (tx == 0)
           *reinterpret_cast<float2*>(po + FR * D + 2 * r) = make_float2(m[mm][i], l[mm][i]);
       }
@@ -181,8 +207,7 @@ __global__ void __launch_bounds__(128) diff_fwd_kernel(const sva_diff_args a, fl
 #pragma unroll
     for (int j = 0; j < RJ; ++j)
       finish4<float>(a, b, h, t, 64 * j + 4 * tx,
-                 make_float4(o[0][i][4 * j], o[0][i][4 * j + 1], o[0][i][4 * j + 2], o[0][i][4 * j + 3]),
-                 make_float4(o[1][i][4 * j], o[1][i][4 * j + 1], o[1][i][4 * j + 2], o[1][i][4 * j + 3]),
+                 quad(o[0][i][2 * j], o[0][i][2 * j + 1]), quad(o[1][i][2 * j], o[1][i][2 * j + 1]),
                  l[0][i], l[1][i], lam);
     if (tx < 2) finish_lse(a, tx, b, h, t, tx == 0 ? m[0][i] : m[1][i], tx == 0 ? l[0][i] : l[1][i]);
   }
@@ -192,7 +217,8 @@ __global__ void __launch_bounds__(128) diff_fwd_kernel(const sva_diff_args a, fl
 // backward
 // ---------------------------------------------------------------------------
 
-constexpr int BR = 64, BS = 32;  // stationary rows and streamed rows of a tile: 256 threads
+// standing and streamed rows of a tile: 256 threads, 4 x 4 scores of a map each
+constexpr int BR = 64, BS = 64;
 
 template <int D>
 constexpr size_t bwd_smem() {
@@ -238,8 +264,8 @@ __global__ void __launch_bounds__(256) diff_bwd_kernel(const sva_diff_args a,
     load_stats(r0);
   }
   const int stream = KV ? (r0 < valid ? a.N : 0) : valid;
-  float acc[4][4 * RJ] = {};             // dQ or dK: columns 64 j + 4 tx + e of the head
-  float accv[KV ? 4 : 1][4 * RJ] = {};   // dV
+  uint64_t acc[4][2 * RJ] = {};            // dQ or dK: columns 64 j + 4 tx + e of the head
+  uint64_t accv[KV ? 4 : 1][2 * RJ] = {};  // dV
   for (int s0 = 0; s0 < stream; s0 += BS) {
     __syncthreads();
     if (KV) {
@@ -251,14 +277,14 @@ __global__ void __launch_bounds__(256) diff_bwd_kernel(const sva_diff_args a,
       load_rows<BS, D>(y2, a.v, a.ldv, b, Nk, h * D, s0, valid);
     }
     __syncthreads();
-    float s1[4][2] = {}, s2[4][2] = {}, dp[4][2] = {};
-    dot_tile<4, 2, M, L, L>(xs, x2, tx, ty, s1);
-    dot_tile<4, 2, M, L, L>(xs + M, x2 + M, tx, ty, s2);
-    dot_tile<4, 2, D, L, L>(ys, y2, tx, ty, dp);
+    float s1[4][BS / 16], s2[4][BS / 16], dp[4][BS / 16];
+    dot_tile<4, BS / 16, M, L, L>(xs, x2, tx, ty, s1);
+    dot_tile<4, BS / 16, M, L, L>(xs + M, x2 + M, tx, ty, s2);
+    dot_tile<4, BS / 16, D, L, L>(ys, y2, tx, ty, dp);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < BS / 16; ++j) {
         const int rr = ty * 4 + i, cc = tx + 16 * j;
         const int qi = KV ? cc : rr;
         const bool ok = (KV ? r0 + rr : s0 + cc) < valid;
@@ -272,30 +298,30 @@ __global__ void __launch_bounds__(256) diff_bwd_kernel(const sva_diff_args a,
     __syncwarp();  // a row of W and dS is written and read by the same half warp
     // dS_1 mixes the first map's half of the columns, dS_2 the second's
     if (RJ == 2) {
-      float half[4][4] = {};
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
+        uint64_t half[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) half[i][e] = acc[i][4 * (RJ - 1) * m + e];
+          for (int e = 0; e < 2; ++e) half[i][e] = acc[i][2 * (RJ - 1) * m + e];
         mix_tile<4, 1, BS, LP, L>(wsm + m * BR * LP, x2 + m * M, tx, ty, half);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][4 * (RJ - 1) * m + e] = half[i][e];
+          for (int e = 0; e < 2; ++e) acc[i][2 * (RJ - 1) * m + e] = half[i][e];
       }
     } else {  // d = 64: columns 4 tx + e; the first eight threads' belong to map 1
-      float one[4][4];
+      uint64_t one[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) one[i][e] = acc[i][e];
+        for (int e = 0; e < 2; ++e) one[i][e] = acc[i][e];
       mix_tile<4, 1, BS, LP, L>(wsm + (tx >= 8 ? BR * LP : 0), x2, tx, ty, one);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = one[i][e];
+        for (int e = 0; e < 2; ++e) acc[i][e] = one[i][e];
     }
     if constexpr (KV) mix_tile<4, RJ, BS, LP, L>(wsm + 2 * BR * LP, y2, tx, ty, accv);
   }
@@ -308,12 +334,12 @@ __global__ void __launch_bounds__(256) diff_bwd_kernel(const sva_diff_args a,
 #pragma unroll
     for (int j = 0; j < RJ; ++j) {
       const int col = h * D + 64 * j + 4 * tx;
-      const float4 v = make_float4(scale * acc[i][4 * j], scale * acc[i][4 * j + 1],
-                                   scale * acc[i][4 * j + 2], scale * acc[i][4 * j + 3]);
+      const float4 x = quad(acc[i][2 * j], acc[i][2 * j + 1]);
+      const float4 v = make_float4(scale * x.x, scale * x.y, scale * x.z, scale * x.w);
       if constexpr (KV) {
         store4(static_cast<float*>(g.dk) + row * g.lddk + col, v);
         store4(static_cast<float*>(g.dv) + row * g.lddv + col,
-               make_float4(accv[i][4 * j], accv[i][4 * j + 1], accv[i][4 * j + 2], accv[i][4 * j + 3]));
+               quad(accv[i][2 * j], accv[i][2 * j + 1]));
       } else {
         store4(static_cast<float*>(g.dq) + row * g.lddq + col, v);
       }
