@@ -1,26 +1,110 @@
-// diff_f32.cu -- the differential softmax anchor in fp32 on the CUDA cores,
-// forward and backward.
+// diff_f32.cu -- the differential softmax anchor in fp32, forward and backward.
 //
-// Forward per query tile: both maps' scores of a key block, one online softmax
-// per map (running maximum and sum in registers), and O_m += P_m V with the
-// block's V read once for both. Backward: the query-stationary and the
-// key-stationary products are the same computation with the two sides
-// exchanged, S^T = K Q^T, dP^T = V dA^T, so one kernel does both; each output
-// has one owner and no atomics are needed. Both maps share dP, and dV needs one
-// product of the combined weights W = P_1 - lambda P_2.
+// Products on the tensor cores with both operands split in two tf32 parts, a = a_hi
+// + a_lo (11 + 11 bits), a b = a_hi b_hi + (a_hi b_lo + a_lo b_hi) + O(2^-22 a b):
+// three MMAs of 16 x 8 x 8, 170 fp32 multiply-adds a cycle and SM where the CUDA
+// cores have 128, and a sixteenth of their instructions (the CUDA-core form of
+// these kernels reached 30% of that rate, bound by operand loads and few warps).
+// The tensor core cuts its sums off (towards minus infinity) instead of rounding
+// them, half a step of bias per MMA, so a chain is kept short: the large and the
+// small products are summed apart, over 64 to 128 channels or 16 rows, and added
+// to the running fp32 sums by the CUDA cores.
+//
+// Forward: 64 query rows a CTA, 16 a warp; keys 16 at a time, both maps' scores,
+// one online softmax each, and O_m += P_m V with V's fragments read once for both.
+// Backward: the query-stationary and the key-stationary products are the same
+// computation with the two sides exchanged, S^T = K Q^T, dP^T = V dA^T, so one
+// kernel does both; each output has one owner and no atomics are needed. Both maps
+// share dP, and dV needs one product of the combined weights W = P_1 - lambda P_2.
+// Scores leave the MMA in the layout that the next one takes as its left operand,
+// up to an exchange of the summed index that the right operand follows: P, W and
+// dS stay in registers.
 #include <algorithm>
-#include <math.h>
 
 #include "diff_common.cuh"
 
 namespace sva {
 namespace {
 
-// Rows [r0, r0 + R) of a [B, n, ld] activation's head columns to shared memory
-// (fp32, row stride D + 4); rows at or behind `valid` are zero.
+// x = hi + lo, each with 11 significant bits: lo is what rounding x to hi left,
+// rounded (off by 2^-22 of x at most)
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+  lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xFFFFE000u;
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+struct FragA {
+  uint32_t hi[4], lo[4];
+};
+struct FragB {
+  uint32_t hi[2], lo[2];
+};
+// sums of one tile: the large products, the small ones
+struct Sum {
+  float big[4], small[4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big[i] = small[i] = 0.f;
+  }
+  __device__ __forceinline__ void add(const FragA& a, const FragB& b) {
+    mma(small, a.lo, b.hi);
+    mma(small, a.hi, b.lo);
+    mma(big, a.hi, b.hi);
+  }
+  __device__ __forceinline__ float at(int i) const { return big[i] + small[i]; }
+};
+
+// A lane's place in a 16 x 8 tile: rows g and g + 8; as a result the columns 2 t and
+// 2 t + 1, as a left operand the summed indexes t and t + 4.
+struct Lane {
+  int g, t;
+  __device__ __forceinline__ Lane() : g(lane_id() >> 2), t(lane_id() & 3) {}
+};
+
+// left operand of rows [r, r + 16), columns [k, k + 8) from split rows of stride L
+template <int L>
+__device__ __forceinline__ void frag_a(FragA& f, const uint32_t* hi, const uint32_t* lo, int r, int k,
+                                       Lane ln) {
+  const int at = (r + ln.g) * L + k + ln.t;
+  f.hi[0] = hi[at]; f.hi[1] = hi[at + 8 * L]; f.hi[2] = hi[at + 4]; f.hi[3] = hi[at + 8 * L + 4];
+  f.lo[0] = lo[at]; f.lo[1] = lo[at + 8 * L]; f.lo[2] = lo[at + 4]; f.lo[3] = lo[at + 8 * L + 4];
+}
+// right operand: rows n..n+7 of x as columns, summed over their columns [k, k + 8)
+template <int L>
+__device__ __forceinline__ void frag_dot(FragB& f, const float* x, int n, int k, Lane ln) {
+  const float* p = x + (n + ln.g) * L + k + ln.t;
+  split(p[0], f.hi[0], f.lo[0]);
+  split(p[4], f.hi[1], f.lo[1]);
+}
+// right operand: columns [n, n + 8) of x, summed over its rows k..k+7 in the order
+// that frag_mix's left operand takes them
+template <int L>
+__device__ __forceinline__ void frag_rows(FragB& f, const float* x, int k, int n, Lane ln) {
+  const float* p = x + (k + 2 * ln.t) * L + n + ln.g;
+  split(p[0], f.hi[0], f.lo[0]);
+  split(p[L], f.hi[1], f.lo[1]);
+}
+// a tile of weights (result layout) as the left operand of a sum over its columns:
+// the columns 2 t and 2 t + 1 take the places t and t + 4
+__device__ __forceinline__ void frag_mix(FragA& f, const float (&c)[4]) {
+  split(c[0], f.hi[0], f.lo[0]);
+  split(c[2], f.hi[1], f.lo[1]);
+  split(c[1], f.hi[2], f.lo[2]);
+  split(c[3], f.hi[3], f.lo[3]);
+}
+
+// Rows [r0, r0 + R) of a [B, n, ld] activation's head columns to shared memory (row
+// stride D + 4); rows at or behind `valid` are zero.
 template <int R, int D>
 __device__ __forceinline__ void load_rows(float* dst, const void* src, int64_t ld, int64_t b, int n,
                                           int col, int r0, int valid) {
+#pragma unroll 4
   for (int i = threadIdx.x; i < R * D / 4; i += blockDim.x) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -28,188 +112,209 @@ __device__ __forceinline__ void load_rows(float* dst, const void* src, int64_t l
     *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
   }
 }
-
-// acc[i][j] = sum_k a[ty*RI + i][k] b[tx + 16 j][k], k < K (row strides LA, LB).
-// The even and the odd k are summed apart, so that a packed fp32 pair takes both.
-template <int RI, int RJ, int K, int LA, int LB>
-__device__ __forceinline__ void dot_tile(const float* a, const float* b, int tx, int ty,
-                                         float (&acc)[RI][RJ]) {
-  uint64_t p[RI][RJ];
-#pragma unroll
-  for (int i = 0; i < RI; ++i)
-#pragma unroll
-    for (int j = 0; j < RJ; ++j) p[i][j] = 0;
-#pragma unroll 4
-  for (int k = 0; k < K; k += 4) {
-    ulonglong2 av[RI], bv[RJ];
-#pragma unroll
-    for (int i = 0; i < RI; ++i)
-      av[i] = *reinterpret_cast<const ulonglong2*>(a + (ty * RI + i) * LA + k);
-#pragma unroll
-    for (int j = 0; j < RJ; ++j)
-      bv[j] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * j) * LB + k);
-#pragma unroll
-    for (int i = 0; i < RI; ++i)
-#pragma unroll
-      for (int j = 0; j < RJ; ++j) {
-        p[i][j] = fma_f2(av[i].x, bv[j].x, p[i][j]);
-        p[i][j] = fma_f2(av[i].y, bv[j].y, p[i][j]);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < RI; ++i)
-#pragma unroll
-    for (int j = 0; j < RJ; ++j) {
-      float lo, hi;
-      f2unpack(p[i][j], lo, hi);
-      acc[i][j] = lo + hi;
-    }
-}
-
-// acc[i][2 j + e] += sum_k p[ty*RI + i][k] x[k][64 j + 4 tx + 2 e, + 1], k < K: pairs of columns
-template <int RI, int RJ, int K, int LP, int LX>
-__device__ __forceinline__ void mix_tile(const float* p, const float* x, int tx, int ty,
-                                         uint64_t (&acc)[RI][2 * RJ]) {
+// the same, split
+template <int R, int D>
+__device__ __forceinline__ void load_split(uint32_t* hi, uint32_t* lo, const void* src, int64_t ld,
+                                           int64_t b, int n, int col, int r0, int valid) {
 #pragma unroll 2
-  for (int k = 0; k < K; k += 4) {
-    float4 pv[RI];
-#pragma unroll
-    for (int i = 0; i < RI; ++i) pv[i] = *reinterpret_cast<const float4*>(p + (ty * RI + i) * LP + k);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-      for (int j = 0; j < RJ; ++j) {
-        const ulonglong2 xv = *reinterpret_cast<const ulonglong2*>(x + (k + kk) * LX + 64 * j + 4 * tx);
-#pragma unroll
-        for (int i = 0; i < RI; ++i) {
-          const float w = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
-          const uint64_t w2 = f2pack(w, w);
-          acc[i][2 * j] = fma_f2(w2, xv.x, acc[i][2 * j]);
-          acc[i][2 * j + 1] = fma_f2(w2, xv.y, acc[i][2 * j + 1]);
-        }
-      }
-    }
+  for (int i = threadIdx.x; i < R * D / 4; i += blockDim.x) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < valid) v = load4(static_cast<const float*>(src) + (b * n + r0 + r) * ld + col + c);
+    uint4 h, l;
+    split(v.x, h.x, l.x);
+    split(v.y, h.y, l.y);
+    split(v.z, h.z, l.z);
+    split(v.w, h.w, l.w);
+    *reinterpret_cast<uint4*>(hi + r * (D + 4) + c) = h;
+    *reinterpret_cast<uint4*>(lo + r * (D + 4) + c) = l;
   }
 }
-__device__ __forceinline__ float4 quad(uint64_t a, uint64_t b) {
-  float4 v;
-  f2unpack(a, v.x, v.y);
-  f2unpack(b, v.z, v.w);
-  return v;
+
+// a row's four lanes
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-__device__ __forceinline__ float row_max16(float v) {
+// s[n] = rows [r, r + 16) of the split x, columns [k0, k0 + K), times rows c + 8 n of y
+template <int K, int L>
+__device__ __forceinline__ void scores(float (&s)[2][4], const uint32_t* hi, const uint32_t* lo,
+                                       const float* y, int r, int c, int k0, Lane ln) {
+  Sum acc[2];
+  acc[0].clear();
+  acc[1].clear();
+#pragma unroll 4
+  for (int k = 0; k < K; k += 8) {
+    FragA a;
+    FragB b[2];
+    frag_a<L>(a, hi, lo, r, k0 + k, ln);
+    frag_dot<L>(b[0], y, c, k0 + k, ln);
+    frag_dot<L>(b[1], y, c + 8, k0 + k, ln);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ float row_sum16(float v) {
+    for (int n = 0; n < 2; ++n) acc[n].add(a, b[n]);
+  }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[n][i] = acc[n].at(i);
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 
-// query rows and keys of a tile: 128 threads, 4 x 4 scores of a map each
-constexpr int FR = kDiffF32Rows, FK = kDiffF32Keys;
+constexpr int FR = kDiffF32Rows, FK = kDiffF32Keys;  // 64 rows: 4 warps; keys of one load
 
 template <int D>
 constexpr size_t fwd_smem() {
-  return (static_cast<size_t>(FR + 2 * FK) * (D + 4) + 2 * FR * (FK + 4)) * sizeof(float);
+  return static_cast<size_t>(2 * FR + 2 * FK) * (D + 4) * sizeof(float);
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) diff_fwd_kernel(const sva_diff_args a, float scale_log2,
-                                                       DiffWork wk) {
-  constexpr int M = D / 2, L = D + 4, LP = FK + 4, RJ = D / 64;
+__global__ void __launch_bounds__(128, 2)
+    diff_fwd_kernel(const __grid_constant__ sva_diff_args a, float scale_log2, DiffWork wk) {
+  constexpr int M = D / 2, L = D + 4, NT = D / 8;
   extern __shared__ __align__(16) float sm[];
-  float* qs = sm;
-  float* ks = qs + FR * L;
+  uint32_t* qhi = reinterpret_cast<uint32_t*>(sm);
+  uint32_t* qlo = qhi + FR * L;
+  float* ks = sm + 2 * FR * L;
   float* vs = ks + FK * L;
-  float* ps = vs + FK * L;  // [2][FR][LP]
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const Lane ln;
+  const int r = warp_id() * 16;
   const DiffUnit u = diff_unit(wk, static_cast<int>(blockIdx.x));
   const int h = u.h, b = u.b;
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const int valid = key_count(a.key_lens, b, Nk);
   const int nkb = (valid + FK - 1) / FK;
-  const int kb0 = u.part < 0 ? 0 : u.part * nkb / wk.split;
-  const int kb1 = u.part < 0 ? nkb : (u.part + 1) * nkb / wk.split;
-  const int q0 = u.q0;
-  load_rows<FR, D>(qs, a.q, a.ldq, b, a.N, h * D, q0, a.N);
-  uint64_t o[2][4][2 * RJ] = {};
-  float m[2][4], l[2][4];
+  const int kb0 = u.part < 0 ? 0 : static_cast<int>(static_cast<int64_t>(u.part) * nkb / wk.split);
+  const int kb1 = u.part < 0 ? nkb : static_cast<int>((u.part + 1LL) * nkb / wk.split);
+  load_split<FR, D>(qhi, qlo, a.q, a.ldq, b, a.N, h * D, u.q0, a.N);
+  float o[2][NT][4];
+  float m[2][2], l[2][2];  // [map][row g, g + 8]
 #pragma unroll
-  for (int mm = 0; mm < 2; ++mm)
+  for (int mp = 0; mp < 2; ++mp) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { m[mm][i] = -INFINITY; l[mm][i] = 0.f; }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[mp][n][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) { m[mp][i] = -INFINITY; l[mp][i] = 0.f; }
+  }
   for (int kb = kb0; kb < kb1; ++kb) {
     __syncthreads();
     load_rows<FK, D>(ks, a.k, a.ldk, b, Nk, h * D, kb * FK, valid);
     load_rows<FK, D>(vs, a.v, a.ldv, b, Nk, h * D, kb * FK, valid);
     __syncthreads();
+#pragma unroll 1
+    for (int c = 0; c < FK; c += 16) {
+      const int left = valid - kb * FK - c;  // keys of these 16 that count
+      if (left <= 0) break;
+      FragA p[2][2];  // [map][8 keys]
 #pragma unroll
-    for (int mm = 0; mm < 2; ++mm) {
-      float s[4][FK / 16];
-      dot_tile<4, FK / 16, M, L, L>(qs + mm * M, ks + mm * M, tx, ty, s);
+      for (int mp = 0; mp < 2; ++mp) {
+        float s[2][4];
+        scores<M, L>(s, qhi, qlo, ks, r, c, mp * M, ln);
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float top = -INFINITY;
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int j = 0; j < FK / 16; ++j) {
-          s[i][j] = kb * FK + tx + 16 * j < valid ? s[i][j] * scale_log2 : -INFINITY;
-          top = fmaxf(top, s[i][j]);
+          for (int i = 0; i < 4; ++i) {
+            s[n][i] = n * 8 + 2 * ln.t + (i & 1) < left ? s[n][i] * scale_log2 : -INFINITY;
+            top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+          }
+        bool grew = false;
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // one of the keys counts at least, so the new maximum is finite
+          const float mx = fmaxf(m[mp][i], row_max(top[i]));
+          f[i] = exp2f(m[mp][i] - mx);
+          grew = grew || mx != m[mp][i];
+          m[mp][i] = mx;
         }
-        // a block holds one valid key at least, so the new maximum is finite
-        const float mx = fmaxf(m[mm][i], row_max16(top));
-        const float f = exp2f(m[mm][i] - mx);
-        m[mm][i] = mx;
-        float* pr = ps + (mm * FR + ty * 4 + i) * LP;
-        float sum = 0.f;
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < FK / 16; ++j) {
-          const float p = exp2f(s[i][j] - mx);
-          pr[tx + 16 * j] = p;
-          sum += p;
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[n][i] = exp2f(s[n][i] - m[mp][i >> 1]);
+            sum[i >> 1] += s[n][i];
+          }
+          frag_mix(p[mp][n], s[n]);
         }
-        l[mm][i] = fmaf(l[mm][i], f, row_sum16(sum));
 #pragma unroll
-        for (int e = 0; e < 2 * RJ; ++e) o[mm][i][e] = mul_f2(o[mm][i][e], f2pack(f, f));
+        for (int i = 0; i < 2; ++i) l[mp][i] = fmaf(l[mp][i], f[i], row_sum(sum[i]));
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mp][n][i] *= f[i >> 1];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        FragB v[2];
+        frag_rows<L>(v[0], vs, c, n * 8, ln);
+        frag_rows<L>(v[1], vs, c + 8, n * 8, ln);
+#pragma unroll
+        for (int mp = 0; mp < 2; ++mp) {
+          Sum acc;
+          acc.clear();
+          acc.add(p[mp][0], v[0]);
+          acc.add(p[mp][1], v[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[mp][n][i] += acc.at(i);
+        }
       }
     }
-    // a row of P is written and read by the same half warp
-    __syncwarp();
-    mix_tile<4, RJ, FK, LP, L>(ps, vs, tx, ty, o[0]);
-    mix_tile<4, RJ, FK, LP, L>(ps + FR * LP, vs, tx, ty, o[1]);
   }
+  // rows g and g + 8, columns 8 n + 2 t and + 1; a whole unit's end takes four
+  // columns a thread, so the outputs go through shared memory
+  __syncthreads();
+  float* os = sm;  // [2 maps][FR][L]: Q's place and more
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = q0 + ty * 4 + i;
-    if (t >= a.N) continue;
+  for (int mp = 0; mp < 2; ++mp)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float2*>(os + (mp * FR + r + ln.g + 8 * i) * L + 8 * n + 2 * ln.t) =
+            make_float2(o[mp][n][2 * i], o[mp][n][2 * i + 1]);
+  float* mls = sm + 2 * FR * L;  // [2 maps][FR][2]
+  if (ln.t == 0)
+#pragma unroll
+    for (int mp = 0; mp < 2; ++mp)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float2*>(mls + 2 * (mp * FR + r + ln.g + 8 * i)) =
+            make_float2(m[mp][i], l[mp][i]);
+  __syncwarp();  // a warp's rows are its own
+  const int lane = lane_id();
+  for (int i = lane; i < 16 * D / 4; i += 32) {
+    const int rr = r + i / (D / 4), c = (i % (D / 4)) * 4, t = u.q0 + rr;
+    if (t >= a.N) break;
+    const float4 x = *reinterpret_cast<const float4*>(os + rr * L + c);
+    const float4 y = *reinterpret_cast<const float4*>(os + (FR + rr) * L + c);
+    const float2 ml1 = *reinterpret_cast<const float2*>(mls + 2 * rr);
+    const float2 ml2 = *reinterpret_cast<const float2*>(mls + 2 * (FR + rr));
     if (u.part >= 0) {
-#pragma unroll
-      for (int mm = 0; mm < 2; ++mm) {
-        float* po = diff_part(wk, D, u.su, u.part, mm);
-        const int r = ty * 4 + i;
-#pragma unroll
-        for (int j = 0; j < RJ; ++j)
-          *reinterpret_cast<float4*>(po + r * D + 64 * j + 4 * tx) =
-              quad(o[mm][i][2 * j], o[mm][i][2 * j + 1]);
-        if (tx == 0)
-          *reinterpret_cast<float2*>(po + FR * D + 2 * r) = make_float2(m[mm][i], l[mm][i]);
+      float* p1 = diff_part(wk, D, u.su, u.part, 0);
+      float* p2 = diff_part(wk, D, u.su, u.part, 1);
+      *reinterpret_cast<float4*>(p1 + rr * D + c) = x;
+      *reinterpret_cast<float4*>(p2 + rr * D + c) = y;
+      if (c == 0) {
+        *reinterpret_cast<float2*>(p1 + FR * D + 2 * rr) = ml1;
+        *reinterpret_cast<float2*>(p2 + FR * D + 2 * rr) = ml2;
       }
-      continue;
+    } else {
+      finish4<float>(a, b, h, t, c, x, y, ml1.y, ml2.y, lambda_of<float>(a, b, t, h));
+      if (c < 8) finish_lse(a, c / 4, b, h, t, c == 0 ? ml1.x : ml2.x, c == 0 ? ml1.y : ml2.y);
     }
-    const float lam = lambda_of<float>(a, b, t, h);
-#pragma unroll
-    for (int j = 0; j < RJ; ++j)
-      finish4<float>(a, b, h, t, 64 * j + 4 * tx,
-                 quad(o[0][i][2 * j], o[0][i][2 * j + 1]), quad(o[1][i][2 * j], o[1][i][2 * j + 1]),
-                 l[0][i], l[1][i], lam);
-    if (tx < 2) finish_lse(a, tx, b, h, t, tx == 0 ? m[0][i] : m[1][i], tx == 0 ? l[0][i] : l[1][i]);
   }
 }
 
@@ -217,131 +322,175 @@ __global__ void __launch_bounds__(128) diff_fwd_kernel(const sva_diff_args a, fl
 // backward
 // ---------------------------------------------------------------------------
 
-// standing and streamed rows of a tile: 256 threads, 4 x 4 scores of a map each
+// standing and streamed rows of a tile. 8 warps: 16 standing rows by half of the
+// streamed ones each; the halves' sums join at the end.
 constexpr int BR = 64, BS = 64;
 
 template <int D>
 constexpr size_t bwd_smem() {
-  return (static_cast<size_t>(2 * BR + 2 * BS) * (D + 4) + 3 * BR * (BS + 4) + 5 * BR) *
-         sizeof(float);
+  return (static_cast<size_t>(4 * BR + 2 * BS) * (D + 4) + kStats * 64) * sizeof(float);
+}
+
+// acc[n] += w (16 rows x 16 streamed ones) times columns n0 + 8 n of x's rows c..c+15
+template <int NT, int L>
+__device__ __forceinline__ void mix(float (&acc)[NT][4], const FragA (&w)[2], const float* x, int c,
+                                    int n0, Lane ln) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    FragB v[2];
+    frag_rows<L>(v[0], x, c, n0 + n * 8, ln);
+    frag_rows<L>(v[1], x, c + 8, n0 + n * 8, ln);
+    Sum s;
+    s.clear();
+    s.add(w[0], v[0]);
+    s.add(w[1], v[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] += s.at(i);
+  }
 }
 
 // KV = false: query rows stand (X = Q, Y = dA), keys stream (X' = K, Y' = V), out dQ.
 // KV = true: key rows stand (X = K, Y = V), queries stream (X' = Q, Y' = dA), out dK, dV.
 template <int D, bool KV>
-__global__ void __launch_bounds__(256) diff_bwd_kernel(const sva_diff_args a,
-                                                       const sva_diff_grads g, DiffBwdScratch ws,
-                                                       float scale) {
-  constexpr int M = D / 2, L = D + 4, LP = BS + 4, RJ = D / 64;
-  constexpr int ST = KV ? BS : BR;  // queries whose statistics a tile needs
+__global__ void __launch_bounds__(256)
+    diff_bwd_kernel(const __grid_constant__ sva_diff_args a, const __grid_constant__ sva_diff_grads g,
+                    DiffBwdScratch ws, float scale) {
+  constexpr int M = D / 2, L = D + 4, NT = D / 8;
   extern __shared__ __align__(16) float sm[];
-  float* xs = sm;
-  float* ys = xs + BR * L;
-  float* x2 = ys + BR * L;
+  uint32_t* xhi = reinterpret_cast<uint32_t*>(sm);
+  uint32_t* xlo = xhi + BR * L;
+  uint32_t* yhi = xlo + BR * L;
+  uint32_t* ylo = yhi + BR * L;
+  float* x2 = sm + 4 * BR * L;
   float* y2 = x2 + BS * L;
-  float* wsm = y2 + BS * L;        // [3][BR][LP]: dS_1, dS_2, W
-  float* stat = wsm + 3 * BR * LP; // [5][ST]: -lse_m log2 e, -delta_m, -lambda
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float* stat = y2 + BS * L;  // [5][64], KV: of the streamed queries
+  const Lane ln;
+  const int r = (warp_id() & 3) * 16, half = warp_id() >> 2;
   const int h = blockIdx.y % a.H, b = blockIdx.y / a.H;
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const int valid = key_count(a.key_lens, b, Nk);
   const int r0 = blockIdx.x * BR;
   const float scale_log2 = scale * kLog2e;
   const int64_t D_all = static_cast<int64_t>(a.H) * D;
-  auto load_stats = [&](int q0) {
-    // q0 is a multiple of 32, so a tile's statistics are one run of a 64-query tile
-    for (int i = threadIdx.x; i < kStats * ST; i += blockDim.x) {
-      const int k = i / ST, c = i % ST;
-      stat[i] = ws.stats[stat_at(static_cast<int>(blockIdx.y), (a.N + 63) / 64, q0 + c) + k * 64];
-    }
-  };
+  const int n_stat_tiles = (a.N + 63) / 64, bh = static_cast<int>(blockIdx.y);
+  float rs[2][kStats] = {};  // queries stand: statistics of rows g, g + 8
   if (KV) {
-    load_rows<BR, D>(xs, a.k, a.ldk, b, Nk, h * D, r0, valid);
-    load_rows<BR, D>(ys, a.v, a.ldv, b, Nk, h * D, r0, valid);
+    load_split<BR, D>(xhi, xlo, a.k, a.ldk, b, Nk, h * D, r0, valid);
+    load_split<BR, D>(yhi, ylo, a.v, a.ldv, b, Nk, h * D, r0, valid);
   } else {
-    load_rows<BR, D>(xs, a.q, a.ldq, b, a.N, h * D, r0, a.N);
-    load_rows<BR, D>(ys, ws.da, D_all, b, a.N, h * D, r0, a.N);
-    load_stats(r0);
+    load_split<BR, D>(xhi, xlo, a.q, a.ldq, b, a.N, h * D, r0, a.N);
+    load_split<BR, D>(yhi, ylo, ws.da, D_all, b, a.N, h * D, r0, a.N);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < kStats; ++k)
+        rs[i][k] = ws.stats[stat_at(bh, n_stat_tiles, r0 + r + ln.g + 8 * i) + 64 * k];
   }
   const int stream = KV ? (r0 < valid ? a.N : 0) : valid;
-  uint64_t acc[4][2 * RJ] = {};            // dQ or dK: columns 64 j + 4 tx + e of the head
-  uint64_t accv[KV ? 4 : 1][2 * RJ] = {};  // dV
+  float acc[NT][4];             // dQ or dK
+  float accv[KV ? NT : 1][4];   // dV
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[n][i] = 0.f;
+      if (KV) accv[KV ? n : 0][i] = 0.f;
+    }
   for (int s0 = 0; s0 < stream; s0 += BS) {
     __syncthreads();
     if (KV) {
       load_rows<BS, D>(x2, a.q, a.ldq, b, a.N, h * D, s0, a.N);
       load_rows<BS, D>(y2, ws.da, D_all, b, a.N, h * D, s0, a.N);
-      load_stats(s0);
+      for (int i = threadIdx.x; i < kStats * 64; i += blockDim.x)
+        stat[i] = ws.stats[stat_at(bh, n_stat_tiles, s0) + i];
     } else {
       load_rows<BS, D>(x2, a.k, a.ldk, b, Nk, h * D, s0, valid);
       load_rows<BS, D>(y2, a.v, a.ldv, b, Nk, h * D, s0, valid);
     }
     __syncthreads();
-    float s1[4][BS / 16], s2[4][BS / 16], dp[4][BS / 16];
-    dot_tile<4, BS / 16, M, L, L>(xs, x2, tx, ty, s1);
-    dot_tile<4, BS / 16, M, L, L>(xs + M, x2 + M, tx, ty, s2);
-    dot_tile<4, BS / 16, D, L, L>(ys, y2, tx, ty, dp);
+#pragma unroll 1
+    for (int c = half * 32; c < half * 32 + 32; c += 16) {
+      if (s0 + c >= stream) break;
+      float p1[2][4], p2[2][4];
+      scores<M, L>(p1, xhi, xlo, x2, r, c, 0, ln);
+      scores<M, L>(p2, xhi, xlo, x2, r, c, M, ln);
+      FragA w[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int n = 0; n < 2; ++n) {
+        float wv[4];
 #pragma unroll
-      for (int j = 0; j < BS / 16; ++j) {
-        const int rr = ty * 4 + i, cc = tx + 16 * j;
-        const int qi = KV ? cc : rr;
-        const bool ok = (KV ? r0 + rr : s0 + cc) < valid;
-        const float p1 = ok ? exp2f(fmaf(s1[i][j], scale_log2, stat[qi])) : 0.f;
-        const float p2 =
-            ok ? stat[4 * ST + qi] * exp2f(fmaf(s2[i][j], scale_log2, stat[ST + qi])) : 0.f;
-        wsm[rr * LP + cc] = p1 * (dp[i][j] + stat[2 * ST + qi]);
-        wsm[(BR + rr) * LP + cc] = p2 * (dp[i][j] + stat[3 * ST + qi]);
-        if (KV) wsm[(2 * BR + rr) * LP + cc] = p1 + p2;
+        for (int i = 0; i < 4; ++i) {
+          const int cc = c + n * 8 + 2 * ln.t + (i & 1);
+          const bool ok = (KV ? r0 + r + ln.g + 8 * (i >> 1) : s0 + cc) < valid;
+          const float n1 = KV ? stat[cc] : rs[i >> 1][0], n2 = KV ? stat[64 + cc] : rs[i >> 1][1];
+          const float nl = KV ? stat[256 + cc] : rs[i >> 1][4];
+          p1[n][i] = ok ? exp2f(fmaf(p1[n][i], scale_log2, n1)) : 0.f;
+          p2[n][i] = ok ? nl * exp2f(fmaf(p2[n][i], scale_log2, n2)) : 0.f;
+          wv[i] = p1[n][i] + p2[n][i];
+        }
+        if (KV) frag_mix(w[n], wv);
       }
-    __syncwarp();  // a row of W and dS is written and read by the same half warp
-    // dS_1 mixes the first map's half of the columns, dS_2 the second's
-    if (RJ == 2) {
+      if constexpr (KV) mix<NT, L>(accv, w, y2, c, 0, ln);
+      float dp[2][4];
+      scores<D, L>(dp, yhi, ylo, y2, r, c, 0, ln);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint64_t half[4][2];
+      for (int mp = 0; mp < 2; ++mp) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int n = 0; n < 2; ++n) {
+          float ds[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) half[i][e] = acc[i][2 * (RJ - 1) * m + e];
-        mix_tile<4, 1, BS, LP, L>(wsm + m * BR * LP, x2 + m * M, tx, ty, half);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) acc[i][2 * (RJ - 1) * m + e] = half[i][e];
+          for (int i = 0; i < 4; ++i) {
+            const int cc = c + n * 8 + 2 * ln.t + (i & 1);
+            const float nd = KV ? stat[(2 + mp) * 64 + cc] : rs[i >> 1][2 + mp];
+            ds[i] = (mp == 0 ? p1[n][i] : p2[n][i]) * (dp[n][i] + nd);
+          }
+          frag_mix(w[n], ds);
+        }
+        // dS_1 mixes the first map's half of the columns, dS_2 the second's
+        mix<NT / 2, L>(reinterpret_cast<float(&)[NT / 2][4]>(acc[mp * NT / 2]), w, x2, c, mp * M, ln);
       }
-    } else {  // d = 64: columns 4 tx + e; the first eight threads' belong to map 1
-      uint64_t one[4][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) one[i][e] = acc[i][e];
-      mix_tile<4, 1, BS, LP, L>(wsm + (tx >= 8 ? BR * LP : 0), x2, tx, ty, one);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) acc[i][e] = one[i][e];
     }
-    if constexpr (KV) mix_tile<4, RJ, BS, LP, L>(wsm + 2 * BR * LP, y2, tx, ty, accv);
   }
+  // the second half's sums to the first, through the tiles' place
+  __syncthreads();
+  constexpr int OUT = KV ? 2 * NT : NT;
+  float4* js = reinterpret_cast<float4*>(sm) + (warp_id() & 3) * 32 * OUT + lane_id();
+  if (half == 1) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      js[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+      if constexpr (KV)
+        js[(NT + n) * 32] = make_float4(accv[n][0], accv[n][1], accv[n][2], accv[n][3]);
+    }
+  }
+  __syncthreads();
+  if (half == 1) return;
   const int n_rows = KV ? Nk : a.N;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty * 4 + i;
-    if (r >= n_rows) continue;
-    const int64_t row = static_cast<int64_t>(b) * n_rows + r;
+  for (int n = 0; n < NT; ++n) {
+    const float4 j = js[n * 32];
+    const float x[4] = {scale * (acc[n][0] + j.x), scale * (acc[n][1] + j.y), scale * (acc[n][2] + j.z),
+                        scale * (acc[n][3] + j.w)};
+    float y[4] = {};
+    if constexpr (KV) {
+      const float4 jv = js[(NT + n) * 32];
+      y[0] = accv[n][0] + jv.x; y[1] = accv[n][1] + jv.y;
+      y[2] = accv[n][2] + jv.z; y[3] = accv[n][3] + jv.w;
+    }
 #pragma unroll
-    for (int j = 0; j < RJ; ++j) {
-      const int col = h * D + 64 * j + 4 * tx;
-      const float4 x = quad(acc[i][2 * j], acc[i][2 * j + 1]);
-      const float4 v = make_float4(scale * x.x, scale * x.y, scale * x.z, scale * x.w);
-      if constexpr (KV) {
-        store4(static_cast<float*>(g.dk) + row * g.lddk + col, v);
-        store4(static_cast<float*>(g.dv) + row * g.lddv + col,
-               quad(accv[i][2 * j], accv[i][2 * j + 1]));
+    for (int i = 0; i < 2; ++i) {
+      const int rr = r0 + r + ln.g + 8 * i;
+      if (rr >= n_rows) continue;
+      const int64_t row = static_cast<int64_t>(b) * n_rows + rr;
+      const int col = h * D + 8 * n + 2 * ln.t;
+      if (KV) {
+        *reinterpret_cast<float2*>(static_cast<float*>(g.dk) + row * g.lddk + col) =
+            make_float2(x[2 * i], x[2 * i + 1]);
+        *reinterpret_cast<float2*>(static_cast<float*>(g.dv) + row * g.lddv + col) =
+            make_float2(y[2 * i], y[2 * i + 1]);
       } else {
-        store4(static_cast<float*>(g.dq) + row * g.lddq + col, v);
+        *reinterpret_cast<float2*>(static_cast<float*>(g.dq) + row * g.lddq + col) =
+            make_float2(x[2 * i], x[2 * i + 1]);
       }
     }
   }
@@ -350,11 +499,10 @@ __global__ void __launch_bounds__(256) diff_bwd_kernel(const sva_diff_args a,
 template <int D>
 cudaError_t fwd(const sva_diff_args& a, void* scratch, cudaStream_t s) {
   const DiffPlan p = diff_plan(a.B, a.N, a.H, a.d, a.n_keys, a.dtype);
-  const DiffWork wk = diff_work(p, a.H, scratch);
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
   cudaError_t e = allow_max_smem<diff_fwd_kernel<D>>();
   if (e != cudaSuccess) return e;
-  diff_fwd_kernel<D><<<p.grid(), 128, fwd_smem<D>(), s>>>(a, scale * kLog2e, wk);
+  diff_fwd_kernel<D><<<p.grid(), 128, fwd_smem<D>(), s>>>(a, scale * kLog2e, diff_work(p, a.H, scratch));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return diff_merge(a, p, scratch, s);
 }
@@ -365,13 +513,16 @@ cudaError_t bwd(const sva_diff_args& a, const sva_diff_grads& g, void* scratch, 
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const unsigned bh = static_cast<unsigned>(a.B * a.H);
-  const int smem = static_cast<int>(bwd_smem<D>());
+  constexpr int smem = static_cast<int>(bwd_smem<D>());
+  static_assert(smem <= kMaxSmem, "shared memory of one CTA");
   cudaError_t e;
   if ((e = allow_max_smem<diff_bwd_kernel<D, false>>()) != cudaSuccess ||
       (e = allow_max_smem<diff_bwd_kernel<D, true>>()) != cudaSuccess)
     return e;
-  diff_bwd_kernel<D, false><<<dim3(static_cast<unsigned>((a.N + BR - 1) / BR), bh), 256, smem, s>>>(a, g, ws, scale);
-  diff_bwd_kernel<D, true><<<dim3(static_cast<unsigned>((Nk + BR - 1) / BR), bh), 256, smem, s>>>(a, g, ws, scale);
+  diff_bwd_kernel<D, true><<<dim3(static_cast<unsigned>((Nk + BR - 1) / BR), bh), 256, smem, s>>>(
+      a, g, ws, scale);
+  diff_bwd_kernel<D, false><<<dim3(static_cast<unsigned>((a.N + BR - 1) / BR), bh), 256, smem, s>>>(
+      a, g, ws, scale);
   return cudaGetLastError();
 }
 

@@ -134,7 +134,7 @@ cudaError_t anchor_f32(const sva_attn_args& a, int* status, cudaStream_t s);
 
 // ---------------------------------------------------------------- differential anchor
 constexpr int kDiffTcRows = 128, kDiffTcKeys = 128;  // bf16: query rows and keys of a tile
-constexpr int kDiffF32Rows = 32, kDiffF32Keys = 64;
+constexpr int kDiffF32Rows = 64, kDiffF32Keys = 32;
 // Units (query tile, head, batch) of a forward call; those of the last partial
 // wave may be cut `split` ways along the keys, with parts in scratch.
 struct DiffPlan {
