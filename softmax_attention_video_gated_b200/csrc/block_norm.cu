@@ -81,16 +81,6 @@ __device__ __forceinline__ void store4n(__nv_bfloat16* p, int n, float4 v) {
   }
 }
 
-// Copies 16 bytes to shared memory in the background, past L1; what lies behind
-// `bytes` becomes zero without being read.
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_upto(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(max(0, min(16, bytes))) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // until at most `stages` - 1 later rows are still on their way
 __device__ __forceinline__ void copy_wait(int stages) {
   switch (stages) {

@@ -29,18 +29,19 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const sva_diff_args a, 
       mx[mm] = fmaxf(mx[mm], diff_part(wk, a.d, su, p, mm)[wk.rows * a.d + 2 * r]);
     o[mm] = make_float4(0.f, 0.f, 0.f, 0.f);
     l[mm] = 0.f;
+#pragma unroll 4
     for (int p = 0; p < wk.split; ++p) {
       const float* po = diff_part(wk, a.d, su, p, mm);
       const float2 ml = *reinterpret_cast<const float2*>(po + wk.rows * a.d + 2 * r);
-      if (ml.x == -INFINITY) continue;  // a part without keys; its O is not written
-      const float w = exp2f(ml.x - mx[mm]);
-      if (4 * lane < a.d) {
-        const float4 x = *reinterpret_cast<const float4*>(po + r * a.d + 4 * lane);
-        o[mm].x = fmaf(w, x.x, o[mm].x);
-        o[mm].y = fmaf(w, x.y, o[mm].y);
-        o[mm].z = fmaf(w, x.z, o[mm].z);
-        o[mm].w = fmaf(w, x.w, o[mm].w);
-      }
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (4 * lane < a.d) x = *reinterpret_cast<const float4*>(po + r * a.d + 4 * lane);
+      // a part without keys has not written its O: whatever is there does not count
+      const bool some = ml.x != -INFINITY;
+      const float w = some ? exp2f(ml.x - mx[mm]) : 0.f;
+      o[mm].x = fmaf(w, some ? x.x : 0.f, o[mm].x);
+      o[mm].y = fmaf(w, some ? x.y : 0.f, o[mm].y);
+      o[mm].z = fmaf(w, some ? x.z : 0.f, o[mm].z);
+      o[mm].w = fmaf(w, some ? x.w : 0.f, o[mm].w);
       l[mm] = fmaf(w, ml.y, l[mm]);
     }
   }
@@ -163,7 +164,7 @@ DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt) {
   if (N <= kDiffFewRows) return p;  // no tiles, no scratch
   const bool tc = dt == SVA_BF16;
   p.rows = tc ? kDiffTcRows : kDiffF32Rows;
-  const int keys = tc ? kDiffTcKeys : kDiffF32Keys;
+  const int keys = tc ? kDiffTcKeys : diff_f32_keys(d);
   const int Nk = n_keys > 0 ? n_keys : N;
   p.n_qtiles = static_cast<int>((N + static_cast<int64_t>(p.rows) - 1) / p.rows);
   const int64_t nkb = (Nk + static_cast<int64_t>(keys) - 1) / keys;

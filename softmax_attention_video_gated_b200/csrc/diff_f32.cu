@@ -100,16 +100,16 @@ __device__ __forceinline__ void frag_mix(FragA& f, const float (&c)[4]) {
 }
 
 // Rows [r0, r0 + R) of a [B, n, ld] activation's head columns to shared memory (row
-// stride D + 4); rows at or behind `valid` are zero.
+// stride D + 4), in the background; rows at or behind `valid` are zero.
 template <int R, int D>
 __device__ __forceinline__ void load_rows(float* dst, const void* src, int64_t ld, int64_t b, int n,
                                           int col, int r0, int valid) {
 #pragma unroll 4
   for (int i = threadIdx.x; i < R * D / 4; i += blockDim.x) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < valid) v = load4(static_cast<const float*>(src) + (b * n + r0 + r) * ld + col + c);
-    *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
+    const bool in = r0 + r < valid;
+    copy16_upto(dst + r * (D + 4) + c,
+                static_cast<const float*>(src) + (b * n + (in ? r0 + r : 0)) * ld + col + c, in ? 16 : 0);
   }
 }
 // the same, split
@@ -168,22 +168,21 @@ __device__ __forceinline__ void scores(float (&s)[2][4], const uint32_t* hi, con
 // forward
 // ---------------------------------------------------------------------------
 
-constexpr int FR = kDiffF32Rows, FK = kDiffF32Keys;  // 64 rows: 4 warps; keys of one load
+constexpr int FR = kDiffF32Rows;  // 4 warps
 
 template <int D>
 constexpr size_t fwd_smem() {
-  return static_cast<size_t>(2 * FR + 2 * FK) * (D + 4) * sizeof(float);
+  return static_cast<size_t>(2 * FR + 4 * diff_f32_keys(D)) * (D + 4) * sizeof(float);
 }
 
 template <int D>
 __global__ void __launch_bounds__(128, 2)
     diff_fwd_kernel(const __grid_constant__ sva_diff_args a, float scale_log2, DiffWork wk) {
-  constexpr int M = D / 2, L = D + 4, NT = D / 8;
+  constexpr int M = D / 2, L = D + 4, NT = D / 8, FK = diff_f32_keys(D);
   extern __shared__ __align__(16) float sm[];
   uint32_t* qhi = reinterpret_cast<uint32_t*>(sm);
   uint32_t* qlo = qhi + FR * L;
-  float* ks = sm + 2 * FR * L;
-  float* vs = ks + FK * L;
+  float* ring = sm + 2 * FR * L;  // two stages of K and V
   const Lane ln;
   const int r = warp_id() * 16;
   const DiffUnit u = diff_unit(wk, static_cast<int>(blockIdx.x));
@@ -205,11 +204,19 @@ __global__ void __launch_bounds__(128, 2)
 #pragma unroll
     for (int i = 0; i < 2; ++i) { m[mp][i] = -INFINITY; l[mp][i] = 0.f; }
   }
+  auto fetch = [&](int kb) {
+    if (kb >= kb1) return;
+    float* st = ring + (kb & 1) * 2 * FK * L;
+    load_rows<FK, D>(st, a.k, a.ldk, b, Nk, h * D, kb * FK, valid);
+    load_rows<FK, D>(st + FK * L, a.v, a.ldv, b, Nk, h * D, kb * FK, valid);
+  };
+  fetch(kb0);
   for (int kb = kb0; kb < kb1; ++kb) {
-    __syncthreads();
-    load_rows<FK, D>(ks, a.k, a.ldk, b, Nk, h * D, kb * FK, valid);
-    load_rows<FK, D>(vs, a.v, a.ldv, b, Nk, h * D, kb * FK, valid);
-    __syncthreads();
+    copy_wait_all();
+    __syncthreads();  // the block is here, and nobody reads the other stage any more
+    fetch(kb + 1);
+    const float* ks = ring + (kb & 1) * 2 * FK * L;
+    const float* vs = ks + FK * L;
 #pragma unroll 1
     for (int c = 0; c < FK; c += 16) {
       const int left = valid - kb * FK - c;  // keys of these 16 that count
@@ -322,13 +329,13 @@ __global__ void __launch_bounds__(128, 2)
 // backward
 // ---------------------------------------------------------------------------
 
-// standing and streamed rows of a tile. 8 warps: 16 standing rows by half of the
-// streamed ones each; the halves' sums join at the end.
-constexpr int BR = 64, BS = 64;
+// standing and streamed rows of a tile. 8 warps: 16 standing rows by a quarter of the
+// streamed ones each; the quarters' sums join at the end. Two stages of streamed rows.
+constexpr int BR = 32, BS = 64;
 
 template <int D>
 constexpr size_t bwd_smem() {
-  return (static_cast<size_t>(4 * BR + 2 * BS) * (D + 4) + kStats * 64) * sizeof(float);
+  return (static_cast<size_t>(4 * BR + 4 * BS) * (D + 4) + 2 * kStats * 64) * sizeof(float);
 }
 
 // acc[n] += w (16 rows x 16 streamed ones) times columns n0 + 8 n of x's rows c..c+15
@@ -352,27 +359,25 @@ __device__ __forceinline__ void mix(float (&acc)[NT][4], const FragA (&w)[2], co
 // KV = false: query rows stand (X = Q, Y = dA), keys stream (X' = K, Y' = V), out dQ.
 // KV = true: key rows stand (X = K, Y = V), queries stream (X' = Q, Y' = dA), out dK, dV.
 template <int D, bool KV>
-__global__ void __launch_bounds__(256)
-    diff_bwd_kernel(const __grid_constant__ sva_diff_args a, const __grid_constant__ sva_diff_grads g,
-                    DiffBwdScratch ws, float scale) {
+__device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_grads& g,
+                                         const DiffBwdScratch& ws, float scale, int tile, int bh,
+                                         float* sm) {
   constexpr int M = D / 2, L = D + 4, NT = D / 8;
-  extern __shared__ __align__(16) float sm[];
   uint32_t* xhi = reinterpret_cast<uint32_t*>(sm);
   uint32_t* xlo = xhi + BR * L;
   uint32_t* yhi = xlo + BR * L;
   uint32_t* ylo = yhi + BR * L;
-  float* x2 = sm + 4 * BR * L;
-  float* y2 = x2 + BS * L;
-  float* stat = y2 + BS * L;  // [5][64], KV: of the streamed queries
+  float* ring = sm + 4 * BR * L;                    // two stages of X', Y'
+  float* stats = ring + 4 * BS * L;                 // and, KV, of the queries' statistics [5][64]
   const Lane ln;
-  const int r = (warp_id() & 3) * 16, half = warp_id() >> 2;
-  const int h = blockIdx.y % a.H, b = blockIdx.y / a.H;
+  const int r = (warp_id() & 1) * 16, quarter = warp_id() >> 1;
+  const int h = bh % a.H, b = bh / a.H;
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const int valid = key_count(a.key_lens, b, Nk);
-  const int r0 = blockIdx.x * BR;
+  const int r0 = tile * BR;
   const float scale_log2 = scale * kLog2e;
   const int64_t D_all = static_cast<int64_t>(a.H) * D;
-  const int n_stat_tiles = (a.N + 63) / 64, bh = static_cast<int>(blockIdx.y);
+  const int n_stat_tiles = (a.N + 63) / 64;
   float rs[2][kStats] = {};  // queries stand: statistics of rows g, g + 8
   if (KV) {
     load_split<BR, D>(xhi, xlo, a.k, a.ldk, b, Nk, h * D, r0, valid);
@@ -396,21 +401,32 @@ __global__ void __launch_bounds__(256)
       acc[n][i] = 0.f;
       if (KV) accv[KV ? n : 0][i] = 0.f;
     }
-  for (int s0 = 0; s0 < stream; s0 += BS) {
-    __syncthreads();
+  auto fetch = [&](int s0) {
+    if (s0 >= stream) return;
+    const int st = (s0 / BS) & 1;
+    float* x2 = ring + st * 2 * BS * L;
+    float* y2 = x2 + BS * L;
     if (KV) {
       load_rows<BS, D>(x2, a.q, a.ldq, b, a.N, h * D, s0, a.N);
       load_rows<BS, D>(y2, ws.da, D_all, b, a.N, h * D, s0, a.N);
-      for (int i = threadIdx.x; i < kStats * 64; i += blockDim.x)
-        stat[i] = ws.stats[stat_at(bh, n_stat_tiles, s0) + i];
+      for (int i = threadIdx.x * 4; i < kStats * 64; i += blockDim.x * 4)
+        copy16(stats + st * kStats * 64 + i, ws.stats + stat_at(bh, n_stat_tiles, s0) + i);
     } else {
       load_rows<BS, D>(x2, a.k, a.ldk, b, Nk, h * D, s0, valid);
       load_rows<BS, D>(y2, a.v, a.ldv, b, Nk, h * D, s0, valid);
     }
-    __syncthreads();
-#pragma unroll 1
-    for (int c = half * 32; c < half * 32 + 32; c += 16) {
-      if (s0 + c >= stream) break;
+  };
+  fetch(0);
+  for (int s0 = 0; s0 < stream; s0 += BS) {
+    copy_wait_all();
+    __syncthreads();  // the block is here, and nobody reads the other stage any more
+    fetch(s0 + BS);
+    const int st = (s0 / BS) & 1;
+    const float* x2 = ring + st * 2 * BS * L;
+    const float* y2 = x2 + BS * L;
+    const float* stat = stats + st * kStats * 64;
+    const int c = quarter * 16;
+    if (s0 + c < stream) {
       float p1[2][4], p2[2][4];
       scores<M, L>(p1, xhi, xlo, x2, r, c, 0, ln);
       scores<M, L>(p2, xhi, xlo, x2, r, c, M, ln);
@@ -451,32 +467,38 @@ __global__ void __launch_bounds__(256)
       }
     }
   }
-  // the second half's sums to the first, through the tiles' place
+  // the other quarters' sums to the first, through the tiles' place, in their order
+  copy_wait_all();
   __syncthreads();
   constexpr int OUT = KV ? 2 * NT : NT;
-  float4* js = reinterpret_cast<float4*>(sm) + (warp_id() & 3) * 32 * OUT + lane_id();
-  if (half == 1) {
+  float4* js = reinterpret_cast<float4*>(sm) + (warp_id() & 1) * 32 * OUT + lane_id();
+  for (int turn = 1; turn < 4; ++turn) {
+    if (quarter == turn) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      js[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-      if constexpr (KV)
-        js[(NT + n) * 32] = make_float4(accv[n][0], accv[n][1], accv[n][2], accv[n][3]);
+      for (int n = 0; n < NT; ++n) {
+        js[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        if constexpr (KV)
+          js[(NT + n) * 32] = make_float4(accv[n][0], accv[n][1], accv[n][2], accv[n][3]);
+      }
     }
+    __syncthreads();
+    if (quarter == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float4 j = js[n * 32];
+        acc[n][0] += j.x; acc[n][1] += j.y; acc[n][2] += j.z; acc[n][3] += j.w;
+        if constexpr (KV) {
+          const float4 jv = js[(NT + n) * 32];
+          accv[n][0] += jv.x; accv[n][1] += jv.y; accv[n][2] += jv.z; accv[n][3] += jv.w;
+        }
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (half == 1) return;
+  if (quarter != 0) return;
   const int n_rows = KV ? Nk : a.N;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const float4 j = js[n * 32];
-    const float x[4] = {scale * (acc[n][0] + j.x), scale * (acc[n][1] + j.y), scale * (acc[n][2] + j.z),
-                        scale * (acc[n][3] + j.w)};
-    float y[4] = {};
-    if constexpr (KV) {
-      const float4 jv = js[(NT + n) * 32];
-      y[0] = accv[n][0] + jv.x; y[1] = accv[n][1] + jv.y;
-      y[2] = accv[n][2] + jv.z; y[3] = accv[n][3] + jv.w;
-    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int rr = r0 + r + ln.g + 8 * i;
@@ -485,15 +507,30 @@ __global__ void __launch_bounds__(256)
       const int col = h * D + 8 * n + 2 * ln.t;
       if (KV) {
         *reinterpret_cast<float2*>(static_cast<float*>(g.dk) + row * g.lddk + col) =
-            make_float2(x[2 * i], x[2 * i + 1]);
-        *reinterpret_cast<float2*>(static_cast<float*>(g.dv) + row * g.lddv + col) =
-            make_float2(y[2 * i], y[2 * i + 1]);
+            make_float2(scale * acc[n][2 * i], scale * acc[n][2 * i + 1]);
+        if constexpr (KV)
+          *reinterpret_cast<float2*>(static_cast<float*>(g.dv) + row * g.lddv + col) =
+              make_float2(accv[n][2 * i], accv[n][2 * i + 1]);
       } else {
         *reinterpret_cast<float2*>(static_cast<float*>(g.dq) + row * g.lddq + col) =
-            make_float2(x[2 * i], x[2 * i + 1]);
+            make_float2(scale * acc[n][2 * i], scale * acc[n][2 * i + 1]);
       }
     }
   }
+}
+
+// Both sides in one launch, the longer tiles (keys stand) first.
+template <int D>
+__global__ void __launch_bounds__(256)
+    diff_bwd_kernel(const __grid_constant__ sva_diff_args a, const __grid_constant__ sva_diff_grads g,
+                    DiffBwdScratch ws, float scale, int key_tiles) {
+  extern __shared__ __align__(16) float sm[];
+  const int heads = a.B * a.H;
+  const int tile = static_cast<int>(blockIdx.x) / heads, bh = static_cast<int>(blockIdx.x) % heads;
+  if (tile < key_tiles)
+    bwd_tile<D, true>(a, g, ws, scale, tile, bh, sm);
+  else
+    bwd_tile<D, false>(a, g, ws, scale, tile - key_tiles, bh, sm);
 }
 
 template <int D>
@@ -512,17 +549,13 @@ cudaError_t bwd(const sva_diff_args& a, const sva_diff_grads& g, void* scratch, 
   const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
-  const unsigned bh = static_cast<unsigned>(a.B * a.H);
   constexpr int smem = static_cast<int>(bwd_smem<D>());
   static_assert(smem <= kMaxSmem, "shared memory of one CTA");
-  cudaError_t e;
-  if ((e = allow_max_smem<diff_bwd_kernel<D, false>>()) != cudaSuccess ||
-      (e = allow_max_smem<diff_bwd_kernel<D, true>>()) != cudaSuccess)
-    return e;
-  diff_bwd_kernel<D, true><<<dim3(static_cast<unsigned>((Nk + BR - 1) / BR), bh), 256, smem, s>>>(
-      a, g, ws, scale);
-  diff_bwd_kernel<D, false><<<dim3(static_cast<unsigned>((a.N + BR - 1) / BR), bh), 256, smem, s>>>(
-      a, g, ws, scale);
+  const cudaError_t e = allow_max_smem<diff_bwd_kernel<D>>();
+  if (e != cudaSuccess) return e;
+  const int key_tiles = (Nk + BR - 1) / BR, query_tiles = (a.N + BR - 1) / BR;
+  diff_bwd_kernel<D><<<static_cast<unsigned>((key_tiles + query_tiles) * a.B * a.H), 256, smem, s>>>(
+      a, g, ws, scale, key_tiles);
   return cudaGetLastError();
 }
 

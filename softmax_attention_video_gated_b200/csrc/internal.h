@@ -134,7 +134,8 @@ cudaError_t anchor_f32(const sva_attn_args& a, int* status, cudaStream_t s);
 
 // ---------------------------------------------------------------- differential anchor
 constexpr int kDiffTcRows = 128, kDiffTcKeys = 128;  // bf16: query rows and keys of a tile
-constexpr int kDiffF32Rows = 64, kDiffF32Keys = 32;
+constexpr int kDiffF32Rows = 64;
+constexpr int diff_f32_keys(int d) { return d > 64 ? 16 : 32; }  // two stages of K and V, two CTAs an SM
 // Units (query tile, head, batch) of a forward call; those of the last partial
 // wave may be cut `split` ways along the keys, with parts in scratch.
 struct DiffPlan {
