@@ -11,9 +11,9 @@
 // Either recomputes the scores: 7/5 of the products of one pass over the pairs,
 // against adding dQ into memory in an order that changes from run to run.
 //
-// 12 warps in three warpgroups: warp 0 TMA, warp 1 TMEM and the scores' MMAs, warp 3
-// the products' MMAs, WG1 and WG2 the weights: thread r of either owns standing row r (its TMEM lane) and 32
-// of the block's 64 columns. The weights' loop is turned by half a step: round i
+// 20 warps in five warpgroups: warp 0 TMA, warp 1 TMEM and the scores' MMAs, warp 3
+// the products' MMAs, the others the weights: thread r of each of four warpgroups owns standing row r (its
+// TMEM lane) and 16 of the block's 64 columns. The weights' loop is turned by half a step: round i
 // makes dS of block i - 1 and P (and W) of block i from dP_{i-1} and S_i, so that
 // the exponentials of one (MUFU) and the products of the other (FMA) fill the same
 // cycles, and neither waits for an MMA that needs what this round makes:
@@ -35,10 +35,13 @@ constexpr int BOXS = 64 * BS * 2;  // [64 columns x 64 rows]
 constexpr int STAGES = 4;
 constexpr int STAGE_BYTES = 4 * BOXS;  // X', Y'
 constexpr int STAT_BYTES = kStats * 64 * 4;
-constexpr int NUM_THREADS = 384;
-constexpr int kWarps = 8;  // that make weights; each arrives once for its 32 rows
+constexpr int WGS = 4;          // warpgroups that make weights, 16 of the block's columns each
+constexpr int kWarps = 4 * WGS;  // each arrives once for its 32 rows
+constexpr int NUM_THREADS = 128 * (1 + WGS);
 constexpr int TMEM_COLS = 512;
-constexpr int kRegsProducer = 56, kRegsWeights = 224;
+// register split: 128 threads at 64 + 512 threads at 104 = 640 threads at 96
+constexpr int kRegsProducer = 64, kRegsWeights = 104;
+constexpr int COLS = BS / WGS;
 // TMEM columns
 constexpr int TM_S = 0;      // S_1, S_2: 64 each
 constexpr int TM_DP = 128;   // dP
@@ -53,8 +56,8 @@ struct Tail {
   uint64_t empty[STAGES];
   uint64_t s_full, dp_full;  // scores in TMEM
   uint64_t loaded;           // ... and in registers
-  uint64_t ds_full[2];       // a warpgroup's dS and W stored
-  uint64_t ds_empty[2];      // ... and used
+  uint64_t ds_full;          // dS and W stored
+  uint64_t ds_empty;         // ... and used
   uint64_t acc_done;
   uint64_t drain[2];
   uint32_t tmem_base;
@@ -112,10 +115,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(&tl->s_full, 1);
     mbar_init(&tl->dp_full, 1);
     mbar_init(&tl->loaded, kWarps);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&tl->ds_full[w], kWarps / 2);
-      mbar_init(&tl->ds_empty[w], 1);
-    }
+    mbar_init(&tl->ds_full, kWarps);
+    mbar_init(&tl->ds_empty, 1);
     mbar_init(&tl->acc_done, 1);
     mbar_init(&tl->drain[0], 1);
     mbar_init(&tl->drain[1], 1);
@@ -258,44 +259,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       constexpr uint32_t idesc_full = idesc_bf16_f32(BR, HD, false, true);      // W Y'
       const uint32_t sm = warp_uniform(desc_lo(smem_u32(smem + L::RING), BOXS));
       const uint32_t wd = warp_uniform(desc_lo(smem_u32(smem + L::W_OFF), 16));
-      // warpgroup w's half of round i: dX += dS_{i-1} X', dV += W_i Y'; st, sp: the
-      // stages of blocks i and i - 1
-      auto products = [&](auto wc, int i, int st, int sp) {
-        constexpr int w = decltype(wc)::value;
-        if (i >= 1) {
-          const uint32_t xb = sm + static_cast<uint32_t>(sp * (STAGE_BYTES >> 4));
-          const uint32_t first = w != 0 || i != 1 ? 1u : 0u;
-          unrolled<BS / 16>([&](auto k) {
-            constexpr int m = decltype(k)::value >> 1, kk = decltype(k)::value & 1;
-            umma_ts_at<m * BOXS + (2 * w + kk) * 2048>(tmem + TM_ACC + 64 * m,
-                                                       tmem + TM_DS + 32 * w + 16 * m + 8 * kk, xb,
-                                                       idesc_half, kk != 0 ? 1u : first);
-          });
-          if (w == 1) umma_commit(&tl->empty[sp]);  // the stage's last use
-        }
-        if (KV && i < n) {
-          const uint32_t yb = sm + static_cast<uint32_t>(st * (STAGE_BYTES >> 4));
-          const uint32_t first = w != 0 || i != 0 ? 1u : 0u;
-          unrolled<BS / 32>([&](auto k) {
-            constexpr int kk = decltype(k)::value;
-            umma_ss_at<(2 * w + kk) * 32, 2 * BOXS + (2 * w + kk) * 2048>(
-                tmem + TM_ACC + HD, wd, yb, idesc_full, kk != 0 ? 1u : first);
-          });
-        }
-        umma_commit(&tl->ds_empty[w]);
-      };
       bool ok = n > 0;
-      int st = 0, sp = STAGES - 1;
+      int st = 0, sp = STAGES - 1;  // stages of blocks i and i - 1
       for (int i = 0; i <= n && ok; ++i) {
-        ok = mma_wait(&tl->ds_full[0], i & 1, abort_flag, status);
+        ok = mma_wait(&tl->ds_full, i & 1, abort_flag, status);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) products(Int<0>(), i, st, sp);
-        __syncwarp();
-        ok = mma_wait(&tl->ds_full[1], i & 1, abort_flag, status);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) products(Int<1>(), i, st, sp);
+        if (elect_one()) {
+          if (i >= 1) {  // dX += dS_{i-1} X', 16 rows of X' (a warpgroup's columns of dS) an MMA
+            const uint32_t xb = sm + static_cast<uint32_t>(sp * (STAGE_BYTES >> 4));
+            const uint32_t more = i != 1 ? 1u : 0u;
+            unrolled<2 * BS / 16>([&](auto k) {
+              constexpr int m = decltype(k)::value & 1, kk = decltype(k)::value >> 1;
+              umma_ts_at<m * BOXS + kk * 2048>(tmem + TM_ACC + 64 * m, tmem + TM_DS + 16 * kk + 8 * m,
+                                               xb, idesc_half, kk != 0 ? 1u : more);
+            });
+            umma_commit(&tl->empty[sp]);  // the stage's last use
+          }
+          if (KV && i < n) {  // dV += W_i Y'
+            const uint32_t yb = sm + static_cast<uint32_t>(st * (STAGE_BYTES >> 4));
+            const uint32_t more = i != 0 ? 1u : 0u;
+            unrolled<BS / 16>([&](auto k) {
+              constexpr int kk = decltype(k)::value;
+              umma_ss_at<kk * 32, 2 * BOXS + kk * 2048>(tmem + TM_ACC + HD, wd, yb, idesc_full,
+                                                        kk != 0 ? 1u : more);
+            });
+          }
+          umma_commit(&tl->ds_empty);
+        }
         __syncwarp();
         sp = st;
         st = st + 1 == STAGES ? 0 : st + 1;
@@ -310,7 +301,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else {
     warpgroup_reg_inc<kRegsWeights>();
     // ------------------------------------------------ weights, then the results
-    const int half = wg - 1;  // this warpgroup's 32 of the block's 64 columns
+    const int part = wg - 1;  // this warpgroup's 16 of the block's 64 columns
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int row = r0 + r;
@@ -318,22 +309,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint64_t scale2 = f2pack(scale_log2, scale_log2);
     uint64_t nlse1 = 0, nlse2 = 0, nd1 = 0, nd2 = 0, nl = 0;  // queries stand: this row's
     if (!KV && n > 0) {
+      // the first two warpgroups bring Q, the others dA, half of the columns each
       const bool in = row < a.N;
+      const int64_t at = static_cast<int64_t>(b) * a.N + row;
+      const __nv_bfloat16* src = part < 2 ? static_cast<const __nv_bfloat16*>(a.q) + at * a.ldq
+                                          : static_cast<const __nv_bfloat16*>(ws.da) + at * a.H * HD;
+      const uint4* p = reinterpret_cast<const uint4*>(src + h * HD + (part & 1) * 64);
       uint32_t x[32];
-      const uint4* src =
-          half == 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                     (static_cast<int64_t>(b) * a.N + row) * a.ldq + h * HD)
-                    : reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(ws.da) +
-                                                     (static_cast<int64_t>(b) * a.N + row) * a.H * HD + h * HD);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 w = in ? src[8 * c + i] : make_uint4(0, 0, 0, 0);
-          x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
-        }
-        tmem_st32(lane_base + TM_X + 64 * half + 32 * c, x);
+      for (int i = 0; i < 8; ++i) {
+        const uint4 w = in ? p[i] : make_uint4(0, 0, 0, 0);
+        x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
       }
+      tmem_st32(lane_base + TM_X + 32 * part, x);
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&tl->x_full);
@@ -347,130 +335,140 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       nl = f2pack(f[4], f[4]);
     }
     bool ok = true;
-    uint64_t p1[16], q2[16];  // P_1 and -lambda P_2 of a block
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p1[i] = q2[i] = 0;
-    const float* stat0 = reinterpret_cast<const float*>(smem + L::STAT) + 32 * half;
+    uint64_t p1[COLS / 2], q2[COLS / 2];  // P_1 and -lambda P_2 of a block
+    const float* stat0 = reinterpret_cast<const float*>(smem + L::STAT) + COLS * part;
+    const float* stat = stat0;  // block i's statistics; prev: block i - 1's
+    const float* prev = stat0 + (STAGES - 1) * (STAT_BYTES / 4);
+    int st = 0;
+    uint32_t phase = 0;  // of full[st]
     for (int i = 0; i <= n && n > 0; ++i) {
-      const float* stat = stat0 + (i % STAGES) * (STAT_BYTES / 4);                   // block i's
-      const float* prev = stat0 + ((i + STAGES - 1) % STAGES) * (STAT_BYTES / 4);  // block i - 1's
-      bool w = true;
-      if (i < n) {
-        // the stage's statistics landed before the scores were made of its rows, but
-        // this thread has to see that copy itself
-        if (KV) w = mbar_wait(&tl->full[i % STAGES], (i / STAGES) & 1, abort_flag, status, WHERE_DIFF_BWD);
-        w = w && mbar_wait(&tl->s_full, i & 1, abort_flag, status, WHERE_DIFF_BWD);
-      }
-      if (i > 0) w = w && mbar_wait(&tl->dp_full, (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
+      uint32_t d1[COLS / 2], d2[COLS / 2], wk[COLS / 2];
+      // dS of the block before first, then this block's scores: fewer values in registers
+      bool w = i == 0 || mbar_wait(&tl->dp_full, (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
       if (!__all_sync(0xffffffffu, w)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t s1[32], s2[32], dp[32];
-      // in the last round the scores are the round's before; nothing made of them is used
-      tmem_ld32(lane_base + TM_S + 32 * half, s1);
-      tmem_ld32(lane_base + TM_S + 64 + 32 * half, s2);
       if (i > 0) {
-        tmem_ld32(lane_base + TM_DP + 32 * half, dp);
-      } else {
+        uint32_t dp[COLS];
+        tmem_ld16(lane_base + TM_DP + COLS * part, dp);
+        tmem_wait_ld();
+        ulonglong2 g1, g2;  // two pairs of queries' statistics at a time
 #pragma unroll
-        for (int k = 0; k < 32; ++k) dp[k] = 0u;
-      }
-      tmem_wait_ld();
-      tc_fence_before();
-      warp_arrive(&tl->loaded);
-      uint32_t d1[16], d2[16], wk[16];
-      ulonglong2 f1, f2, f3, g1, g2;  // two pairs of queries' statistics at a time
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (KV) {
-          if (k % 2 == 0) {
-            g1 = *reinterpret_cast<const ulonglong2*>(prev + 128 + 2 * k);
-            g2 = *reinterpret_cast<const ulonglong2*>(prev + 192 + 2 * k);
-            f1 = *reinterpret_cast<const ulonglong2*>(stat + 2 * k);
-            f2 = *reinterpret_cast<const ulonglong2*>(stat + 64 + 2 * k);
-            f3 = *reinterpret_cast<const ulonglong2*>(stat + 256 + 2 * k);
+        for (int k = 0; k < COLS / 2; ++k) {
+          if (KV) {
+            if (k % 2 == 0) {
+              g1 = *reinterpret_cast<const ulonglong2*>(prev + 128 + 2 * k);
+              g2 = *reinterpret_cast<const ulonglong2*>(prev + 192 + 2 * k);
+            }
+            nd1 = k % 2 == 0 ? g1.x : g1.y;
+            nd2 = k % 2 == 0 ? g2.x : g2.y;
           }
-          nd1 = k % 2 == 0 ? g1.x : g1.y;
-          nd2 = k % 2 == 0 ? g2.x : g2.y;
-          nlse1 = k % 2 == 0 ? f1.x : f1.y;
-          nlse2 = k % 2 == 0 ? f2.x : f2.y;
-          nl = k % 2 == 0 ? f3.x : f3.y;
+          float x0, x1, y0, y1;
+          const uint64_t dpp = f2pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1]));
+          f2unpack(mul_f2(p1[k], add_f2(dpp, nd1)), x0, x1);
+          f2unpack(mul_f2(q2[k], add_f2(dpp, nd2)), y0, y1);
+          d1[k] = pack_bf16x2(x0, x1);
+          d2[k] = pack_bf16x2(y0, y1);
         }
-        float x0, x1, y0, y1;
-        const uint64_t dpp = f2pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1]));
-        f2unpack(mul_f2(p1[k], add_f2(dpp, nd1)), x0, x1);
-        f2unpack(mul_f2(q2[k], add_f2(dpp, nd2)), y0, y1);
-        d1[k] = pack_bf16x2(x0, x1);
-        d2[k] = pack_bf16x2(y0, y1);
-        f2unpack(fma_f2(f2pack(__uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1])), scale2,
-                        nlse1), x0, x1);
-        f2unpack(fma_f2(f2pack(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])), scale2,
-                        nlse2), y0, y1);
-        p1[k] = f2pack(ex2_mufu(x0), ex2_mufu(x1));
-        q2[k] = mul_f2(f2pack(ex2_mufu(y0), ex2_mufu(y1)), nl);
-        if (KV) {
-          f2unpack(add_f2(p1[k], q2[k]), x0, x1);
-          wk[k] = pack_bf16x2(x0, x1);
+        if (!KV) {  // keys of block i - 1 that count
+          const int left = valid - (i - 1) * BS - COLS * part;
+          if (left < COLS) {
+#pragma unroll
+            for (int k = 0; k < COLS / 2; ++k) {
+              const uint32_t keep = (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
+              d1[k] &= keep;
+              d2[k] &= keep;
+            }
+          }
         }
       }
-      if (!KV) {  // keys of block i - 1 that count; of block 0's, none behind
-        const int left = valid - (i - 1) * BS - 32 * half;
-        if (left < 32) {
+      if (i < n) {
+        // the stage's statistics landed before the scores were made of its rows, but
+        // this thread has to see that copy itself
+        w = !KV || mbar_wait(&tl->full[st], phase, abort_flag, status, WHERE_DIFF_BWD);
+        w = w && mbar_wait(&tl->s_full, i & 1, abort_flag, status, WHERE_DIFF_BWD);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s1[COLS], s2[COLS];
+        tmem_ld16(lane_base + TM_S + COLS * part, s1);
+        tmem_ld16(lane_base + TM_S + 64 + COLS * part, s2);
+        tmem_wait_ld();
+        tc_fence_before();
+        warp_arrive(&tl->loaded);
+        ulonglong2 f1, f2, f3;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint32_t keep = (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
-            d1[k] &= keep;
-            d2[k] &= keep;
+        for (int k = 0; k < COLS / 2; ++k) {
+          if (KV) {
+            if (k % 2 == 0) {
+              f1 = *reinterpret_cast<const ulonglong2*>(stat + 2 * k);
+              f2 = *reinterpret_cast<const ulonglong2*>(stat + 64 + 2 * k);
+              f3 = *reinterpret_cast<const ulonglong2*>(stat + 256 + 2 * k);
+            }
+            nlse1 = k % 2 == 0 ? f1.x : f1.y;
+            nlse2 = k % 2 == 0 ? f2.x : f2.y;
+            nl = k % 2 == 0 ? f3.x : f3.y;
+          }
+          float x0, x1, y0, y1;
+          f2unpack(fma_f2(f2pack(__uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1])), scale2,
+                          nlse1), x0, x1);
+          f2unpack(fma_f2(f2pack(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])), scale2,
+                          nlse2), y0, y1);
+          p1[k] = f2pack(ex2_mufu(x0), ex2_mufu(x1));
+          q2[k] = mul_f2(f2pack(ex2_mufu(y0), ex2_mufu(y1)), nl);
+          if (KV) {
+            f2unpack(add_f2(p1[k], q2[k]), x0, x1);
+            wk[k] = pack_bf16x2(x0, x1);
           }
         }
       }
       // the products of the round before have used dS and W
-      w = i == 0 || mbar_wait(&tl->ds_empty[half], (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
+      w = i == 0 || mbar_wait(&tl->ds_empty, (i - 1) & 1, abort_flag, status, WHERE_DIFF_BWD);
       if (!__all_sync(0xffffffffu, w)) {
         ok = false;
         break;
       }
       tc_fence_after();
       if (i > 0) {
-        tmem_st16(lane_base + TM_DS + 32 * half, d1);
-        tmem_st16(lane_base + TM_DS + 32 * half + 16, d2);
+        tmem_st8(lane_base + TM_DS + COLS * part, d1);
+        tmem_st8(lane_base + TM_DS + COLS * part + COLS / 2, d2);
       }
       if (KV && i < n) {
         // row r of W, 128-byte swizzle: chunk c of the row at c ^ (r & 7)
         uint8_t* wrow = smem + L::W_OFF + r * 128;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(wrow + (((4 * half + c) ^ (r & 7)) << 4)) =
+        for (int c = 0; c < COLS / 8; ++c)
+          *reinterpret_cast<uint4*>(wrow + (((COLS / 8 * part + c) ^ (r & 7)) << 4)) =
               make_uint4(wk[4 * c], wk[4 * c + 1], wk[4 * c + 2], wk[4 * c + 3]);
         fence_proxy_async_smem();
       }
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(&tl->ds_full[half]);
+      warp_arrive(&tl->ds_full);
+      prev = stat;
+      st = st + 1 == STAGES ? 0 : st + 1;
+      phase ^= st == 0 ? 1u : 0u;
+      stat = stat0 + st * (STAT_BYTES / 4);
     }
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(&tl->acc_done, 0, abort_flag, status, WHERE_DIFF_BWD));
     tc_fence_after();
-    // keys stand: WG1 writes dK, WG2 dV, all 128 columns; queries stand: half of dQ each
+    // keys stand: half of dK or dV a warpgroup; queries stand: a quarter of dQ
     const int64_t at = static_cast<int64_t>(b) * n_rows + row;
     __nv_bfloat16* dst;
-    int col0, ncols;
-    float f;
-    if (KV) {
-      dst = half == 0 ? static_cast<__nv_bfloat16*>(g.dk) + at * g.lddk
-                      : static_cast<__nv_bfloat16*>(g.dv) + at * g.lddv;
-      col0 = TM_ACC + HD * half;
-      ncols = HD;
-      f = half == 0 ? scale : 1.0f;
-    } else {
-      dst = static_cast<__nv_bfloat16*>(g.dq) + at * g.lddq + 64 * half;
-      col0 = TM_ACC + 64 * half;
-      ncols = 64;
-      f = scale;
-    }
+    constexpr int ncols = KV ? 64 : 32;
+    if (KV)
+      dst = (part < 2 ? static_cast<__nv_bfloat16*>(g.dk) + at * g.lddk
+                      : static_cast<__nv_bfloat16*>(g.dv) + at * g.lddv) + (part & 1) * 64;
+    else
+      dst = static_cast<__nv_bfloat16*>(g.dq) + at * g.lddq + 32 * part;
     dst += h * HD;
+    const int col0 = TM_ACC + ncols * part;
+    const float f = KV && part >= 2 ? 1.0f : scale;
     const bool zero = n == 0 || (KV && row >= valid);
 #pragma unroll 1
     for (int c = 0; c < ncols && ok; c += 32) {
