@@ -26,11 +26,12 @@
 namespace sva {
 namespace {
 
-// x = hi + lo, each with 11 significant bits: lo is what rounding x to hi left,
-// rounded (off by 2^-22 of x at most)
+// x = hi + lo, each with 11 significant bits: hi is x rounded, lo what that left, cut
+// off behind a factor of 1 + 2^-11.5 that stands for the mean half step (rounding its
+// bits as hi's would turn a NaN into a zero; as it is the NaN stays in lo)
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
-  lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xFFFFE000u;
+  lo = __float_as_uint((x - __uint_as_float(hi)) * 1.00034527f) & 0xFFFFE000u;
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm(

@@ -370,8 +370,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int i = 0; i < 16; ++i) {
           float x0, x1;
           f2unpack(fma_f2(f2pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), scale2, negm2), x0, x1);
-          const float p0 = ex2_mufu(x0);
-          const float p1 = ex2_mufu(x1);
+          float p0, p1;
+          // a quarter on the FMA pipe: 8190 tokens, 16 heads 823 -> 772 us (an eighth: 804,
+          // half: 793)
+          if (i % 4 == 3) {
+            ex2_poly2(x0, x1, p0, p1);
+          } else {
+            p0 = ex2_mufu(x0);
+            p1 = ex2_mufu(x1);
+          }
           acc2[i & 3] = add_f2(acc2[i & 3], f2pack(p0, p1));
           pk[i] = pack_bf16x2(p0, p1);
         }

@@ -220,6 +220,19 @@ def test_flat_and_peaked_maps(dtype, q_scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 8])
+def test_nan_among_the_keys_is_not_lost(dtype, N):
+    # a key that counts and is not a number leaves no finite result, wherever it stands in a block
+    x = make(1, N, 160, 1, 128, dtype, 51)
+    t = dev(x, dtype)
+    for at in (0, 3, 6, 7, 70, 127, 128, 159):
+        k = t["k"].clone()
+        k[0, at] = float("nan")
+        out, _ = forward({**t, "k": k}, 1)
+        assert not torch.isfinite(out.float()).any(), at
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_slices_of_wider_buffers(dtype):
     # q, k, v, gate, lambda and their gradients as column slices of one buffer, the result in
     # another's: what lies between is left as it was
