@@ -3,7 +3,7 @@
 // and the row sums delta_m (diff_aux.cu):
 //     W = P_1 - lambda P_2,  dS_1 = P_1 (dP - delta_1),  dS_2 = -lambda P_2 (dP - delta_2)
 //     dV = W^T dA,  dK_m = scale dS_m^T Q_m,  dQ_m = scale dS_m K_m
-// Two kernels of one shape, so that every output has one owner and its sum one
+// Two passes of one shape, so that every output has one owner and its sum one
 // order (no atomics): 128 rows X, Y stand, blocks of 64 rows X', Y' stream by.
 //     keys stand:    X, Y = K, V   X', Y' = Q, dA   S^T = K Q^T, dP^T = V dA^T;
 //                    out dK = dS^T Q, dV = W^T dA
@@ -80,22 +80,20 @@ __device__ __forceinline__ bool mma_wait(uint64_t* bar, int parity, volatile int
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, WHERE_DIFF_BWD));
 }
 
+struct Maps {  // boxes of 128 standing rows of K and V; of 64 streamed rows of each
+  CUtensorMap k_stand, v_stand, k, v, q, da;
+};
+
 template <bool KV>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
-    diff_bwd_tc_kernel(const __grid_constant__ CUtensorMap map_x,
-                       const __grid_constant__ CUtensorMap map_y,
-                       const __grid_constant__ CUtensorMap map_x2,
-                       const __grid_constant__ CUtensorMap map_y2,
-                       const __grid_constant__ sva_diff_args a,
-                       const __grid_constant__ sva_diff_grads g, DiffBwdScratch ws, int n_tiles,
-                       float scale, int* status) {
+__device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& a,
+                                         const sva_diff_grads& g, const DiffBwdScratch& ws, int tile,
+                                         int bh, float scale, int* status, uint8_t* smem_raw) {
+  const CUtensorMap &map_x = maps.k_stand, &map_y = maps.v_stand;  // Q and dA stand in TMEM, loaded by threads
+  const CUtensorMap &map_x2 = KV ? maps.q : maps.k, &map_y2 = KV ? maps.da : maps.v;
   using L = Layout<KV>;
-  extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   Tail* tl = reinterpret_cast<Tail*>(smem + L::TAIL);
-  const int tile = static_cast<int>(blockIdx.x) % n_tiles;
-  const int bh = static_cast<int>(blockIdx.x) / n_tiles;
   const int h = bh % a.H, b = bh / a.H;
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const int valid = key_count(a.key_lens, b, Nk);
@@ -500,28 +498,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-template <bool KV>
-cudaError_t launch(const sva_diff_args& a, const sva_diff_grads& g, const DiffBwdScratch& ws,
-                   float scale, int* status, cudaStream_t s) {
-  const int D = a.H * a.d;
-  const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
-  CUtensorMap mx, my, mx2, my2;
-  bool ok;
-  if (KV) {
-    ok = diff_map(&mx, a.k, a.ldk, a.B, Nk, D, BR) && diff_map(&my, a.v, a.ldv, a.B, Nk, D, BR) &&
-         diff_map(&mx2, a.q, a.ldq, a.B, a.N, D, BS) && diff_map(&my2, ws.da, D, a.B, a.N, D, BS);
+// Both sides in one launch, the longer tiles (keys stand) first: the second fills the
+// first's last wave.
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    diff_bwd_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ sva_diff_args a,
+                       const __grid_constant__ sva_diff_grads g, DiffBwdScratch ws, int key_tiles,
+                       int query_tiles, float scale, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  int cta = static_cast<int>(blockIdx.x);
+  const int n_key = key_tiles * a.B * a.H;
+  if (cta < n_key) {
+    bwd_tile<true>(maps, a, g, ws, cta % key_tiles, cta / key_tiles, scale, status, smem_raw);
   } else {
-    ok = diff_map(&mx2, a.k, a.ldk, a.B, Nk, D, BS) && diff_map(&my2, a.v, a.ldv, a.B, Nk, D, BS);
-    mx = mx2;  // Q and dA go to TMEM by the threads' own loads
-    my = my2;
+    cta -= n_key;
+    bwd_tile<false>(maps, a, g, ws, cta % query_tiles, cta / query_tiles, scale, status, smem_raw);
   }
-  if (!ok) return cudaErrorInvalidValue;
-  const int n_tiles = ((KV ? Nk : a.N) + BR - 1) / BR;
-  const cudaError_t e = allow_max_smem<diff_bwd_tc_kernel<KV>>();
-  if (e != cudaSuccess) return e;
-  diff_bwd_tc_kernel<KV><<<static_cast<unsigned>(n_tiles * a.B * a.H), NUM_THREADS, Layout<KV>::SMEM, s>>>(
-      mx, my, mx2, my2, a, g, ws, n_tiles, scale, status);
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -530,8 +521,21 @@ cudaError_t diff_bwd_bf16(const sva_diff_args& a, const sva_diff_grads& g, int* 
                           void* scratch, cudaStream_t s) {
   const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(HD / 2));
-  const cudaError_t e = launch<true>(a, g, ws, scale, status, s);
-  return e != cudaSuccess ? e : launch<false>(a, g, ws, scale, status, s);
+  const int D = a.H * a.d;
+  const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
+  Maps m;
+  if (!diff_map(&m.k_stand, a.k, a.ldk, a.B, Nk, D, BR) ||
+      !diff_map(&m.v_stand, a.v, a.ldv, a.B, Nk, D, BR) || !diff_map(&m.k, a.k, a.ldk, a.B, Nk, D, BS) ||
+      !diff_map(&m.v, a.v, a.ldv, a.B, Nk, D, BS) || !diff_map(&m.q, a.q, a.ldq, a.B, a.N, D, BS) ||
+      !diff_map(&m.da, ws.da, D, a.B, a.N, D, BS))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = allow_max_smem<diff_bwd_tc_kernel>();
+  if (e != cudaSuccess) return e;
+  const int key_tiles = (Nk + BR - 1) / BR, query_tiles = (a.N + BR - 1) / BR;
+  constexpr size_t smem = Layout<true>::SMEM > Layout<false>::SMEM ? Layout<true>::SMEM : Layout<false>::SMEM;
+  diff_bwd_tc_kernel<<<static_cast<unsigned>((key_tiles + query_tiles) * a.B * a.H), NUM_THREADS, smem, s>>>(
+      m, a, g, ws, key_tiles, query_tiles, scale, status);
+  return cudaGetLastError();
 }
 
 }  // namespace sva

@@ -168,5 +168,11 @@ __device__ __forceinline__ float* diff_part(const DiffWork& wk, int d, int su, i
          ((static_cast<int64_t>(su) * wk.split + part) * 2 + map) * wk.rows * (d + 2);
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
 }  // namespace
 }  // namespace sva
