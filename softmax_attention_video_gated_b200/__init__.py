@@ -225,9 +225,15 @@ def _check(status: int, where: str) -> None:
 # tensor marshalling
 # ---------------------------------------------------------------------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _dtype_code(t) -> int:
@@ -394,49 +400,68 @@ _NULL = (None, 0)
 def _lead(t):
     """(dtype, its code, device index) of a call, from its leading tensor; the kernels run on the
     current device."""
-    dev = t.get_device()
-    torch = _torch()
+    dt, dev = t.dtype, t.get_device()
     if dev < 0:
         raise ValueError("expected a CUDA tensor")
-    if dev != torch._C._cuda_getDevice():
+    if dev != _cuda().device():
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
-    return t.dtype, _dtype_code(t), dev
+    return dt, _dtype_code(t), dev
+
+
+class _Cuda:
+    """torch's raw device and stream queries (the Python ones take as long as a small kernel)."""
+
+    def __init__(self):
+        c = _torch()._C
+        self.device, self.stream = c._cuda_getDevice, c._cuda_getCurrentRawStream
+
+
+_CUDA = None
+
+
+def _cuda() -> _Cuda:
+    global _CUDA
+    if _CUDA is None:
+        _CUDA = _Cuda()
+    return _CUDA
 
 
 def _here(stream, dev: int) -> int:
     """The call's stream: the given one, or the current one of its device."""
-    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if stream is not None else _cuda().stream(dev)
+
+
+def _refuse(t, dt, dev: int, name: str, want: str):
+    """The error for a tensor that does not fit."""
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    raise ValueError(f"expected {name} {want}, got {tuple(t.shape)} with strides {tuple(t.stride())}")
 
 
 def _act(t, B: int, N: int, W: int, dt, dev: int, name: str):
     """(address, row stride) of an activation [B, N, >=W]; (None, 0) for None."""
     if t is None:
         return _NULL
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != B or shape[1] != N or shape[2] < W:
-        raise ValueError(f"expected {name} [B={B}, N={N}, >={W}], got {tuple(shape)}")
-    # a single row's stride is not used: a rounded one keeps it valid for odd widths
-    ld = stride[1] if N > 1 else stride[0] if B > 1 else (max(stride[1], W) + 7) // 8 * 8
-    if (stride[2] != 1 and W > 1) or (B > 1 and stride[0] != N * ld):
-        raise ValueError(f"{name}: rows must be unit-stride with batches N*ld apart")
-    if t.dtype is not dt:
-        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    return t.data_ptr(), ld
+    if t.dtype is dt and t.get_device() == dev and t.ndim == 3:
+        b, n, w = t.shape
+        if b == B and n == N and w >= W:
+            sb, ld, one = t.stride()
+            if N == 1:  # a single row's stride is not used: a rounded one serves odd widths
+                ld = sb if B > 1 else (max(ld, W) + 7) // 8 * 8
+            if (one == 1 or W == 1) and (sb == N * ld or B == 1):
+                return t.data_ptr(), ld
+    _refuse(t, dt, dev, name, f"[B={B}, N={N}, >={W}] of unit-stride rows, batches N*ld apart")
 
 
 def _flat(t, shape: tuple, dt, dev: int, name: str):
     """Address of a contiguous tensor of this shape; None for None."""
     if t is None:
         return None
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"expected {name} contiguous {shape}, got {tuple(t.shape)}")
-    if t.dtype is not dt:
-        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    return t.data_ptr()
+    if t.dtype is dt and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dt, dev, name, f"contiguous {shape}")
 
 
 def _lam(lam, B: int, N: int, H: int, dt, dev: int, name: str):
@@ -521,17 +546,13 @@ def _batch_rows(t, B: int, D: int, dt, dev: int, name: str):
     """(address, row stride) of a per-batch modulation [B, >=D]; (None, 0) for None."""
     if t is None:
         return _NULL
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != B or shape[1] < D or (stride[1] != 1 and D > 1):
-        raise ValueError(f"expected {name} [B={B}, >={D}] of unit-stride rows, got {tuple(shape)}")
-    if t.dtype is not dt:
-        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    if B > 1:
-        return t.data_ptr(), stride[0]
-    # one row: any stride does, a rounded one keeps it valid for odd widths
-    return t.data_ptr(), (D + 7) // 8 * 8
+    if t.dtype is dt and t.get_device() == dev and t.ndim == 2:
+        b, w = t.shape
+        ld, one = t.stride()
+        if b == B and w >= D and (one == 1 or D == 1):
+            # one row: its stride is not used, a rounded one serves odd widths
+            return t.data_ptr(), ld if B > 1 else (D + 7) // 8 * 8
+    _refuse(t, dt, dev, name, f"[B={B}, >={D}] of unit-stride rows")
 
 
 def _norm_args(h, o, w_post, gate, h_out, w_pre, scale, shift, u, kind, eps, res_scale, stats):
