@@ -76,7 +76,9 @@ __device__ __forceinline__ float half_sum(float v) {
 template <typename T, int Q>
 __global__ void __launch_bounds__(256)
     diff_prep_kernel(const __grid_constant__ sva_diff_args a, const __grid_constant__ sva_diff_grads g,
-                     DiffBwdScratch ws) {
+                     DiffBwdScratch ws, int* status) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < SVA_STATUS_BYTES / 4)
+    status[threadIdx.x] = 0;  // for the kernel behind
   const int lane = lane_id(), l16 = lane & 15;
   const int h = static_cast<int>(blockIdx.y) * 8 + warp_id(), b = static_cast<int>(blockIdx.z);
   if (h >= a.H) return;
@@ -125,7 +127,10 @@ __global__ void __launch_bounds__(256)
     // an empty row's -infinity stays, a rounded-up token has it: their weights come
     // out as 2^-inf = 0
     float v = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-    if (l16 >= 2) v = !in ? 0.f : l16 == 2 ? -d1 : l16 == 3 ? -d2 : -lam;
+    // a sigmoid's lambda is positive and goes into the second map's exponent
+    const bool raw = (a.flags & SVA_FLAG_LAMBDA_VALUE) != 0;
+    if (l16 == 1 && !raw) v += log2f(lam);
+    if (l16 >= 2) v = !in ? 0.f : l16 == 2 ? -d1 : l16 == 3 ? -d2 : raw ? -lam : -1.f;
     ws.stats[stat_at(bh, (a.N + 63) / 64, t) + l16 * 64] = v;
   }
   if (l16 == 0 && in) {
@@ -164,14 +169,14 @@ __global__ void __launch_bounds__(1024) diff_dlam_kernel(const __grid_constant__
 
 template <typename T>
 cudaError_t prepare(const sva_diff_args& a, const sva_diff_grads& g, const DiffBwdScratch& ws,
-                    cudaStream_t s) {
+                    int* status, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.N + 63) / 64 * 32), static_cast<unsigned>((a.H + 7) / 8),
                   static_cast<unsigned>(a.B));
   constexpr bool kHalf = sizeof(T) == 4;  // fp32 heads may be of 64
   if (kHalf && a.d == 64)
-    diff_prep_kernel<T, kHalf ? 1 : 2><<<grid, 256, 0, s>>>(a, g, ws);
+    diff_prep_kernel<T, kHalf ? 1 : 2><<<grid, 256, 0, s>>>(a, g, ws, status);
   else
-    diff_prep_kernel<T, 2><<<grid, 256, 0, s>>>(a, g, ws);
+    diff_prep_kernel<T, 2><<<grid, 256, 0, s>>>(a, g, ws, status);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.ldl != 0) return e;
   diff_dlam_kernel<T><<<static_cast<unsigned>(a.H), 1024, 0, s>>>(a, g, ws);
@@ -247,7 +252,7 @@ cudaError_t diff_bwd(const sva_diff_args& a, const sva_diff_grads& g, int* statu
                      cudaStream_t s) {
   const bool tc = a.dtype == SVA_BF16;
   const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
-  const cudaError_t e = tc ? prepare<__nv_bfloat16>(a, g, ws, s) : prepare<float>(a, g, ws, s);
+  const cudaError_t e = tc ? prepare<__nv_bfloat16>(a, g, ws, status, s) : prepare<float>(a, g, ws, status, s);
   if (e != cudaSuccess) return e;
   return tc ? diff_bwd_bf16(a, g, status, scratch, s) : diff_bwd_f32(a, g, scratch, s);
 }

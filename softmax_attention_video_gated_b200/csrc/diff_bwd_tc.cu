@@ -332,6 +332,8 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
       nd2 = f2pack(f[3], f[3]);
       nl = f2pack(f[4], f[4]);
     }
+    const uint64_t minus_one = f2pack(-1.f, -1.f);
+    const bool raw = (a.flags & SVA_FLAG_LAMBDA_VALUE) != 0;  // else the last statistic is -1
     bool ok = true;
     uint64_t p1[COLS / 2], q2[COLS / 2];  // P_1 and -lambda P_2 of a block
     const float* stat0 = reinterpret_cast<const float*>(smem + L::STAT) + COLS * part;
@@ -398,14 +400,14 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
         tmem_wait_ld();
         tc_fence_before();
         warp_arrive(&tl->loaded);
-        ulonglong2 f1, f2, f3;
+        ulonglong2 f1, f2, f3 = {minus_one, minus_one};
 #pragma unroll
         for (int k = 0; k < COLS / 2; ++k) {
           if (KV) {
             if (k % 2 == 0) {
               f1 = *reinterpret_cast<const ulonglong2*>(stat + 2 * k);
               f2 = *reinterpret_cast<const ulonglong2*>(stat + 64 + 2 * k);
-              f3 = *reinterpret_cast<const ulonglong2*>(stat + 256 + 2 * k);
+              if (raw) f3 = *reinterpret_cast<const ulonglong2*>(stat + 256 + 2 * k);
             }
             nlse1 = k % 2 == 0 ? f1.x : f1.y;
             nlse2 = k % 2 == 0 ? f2.x : f2.y;

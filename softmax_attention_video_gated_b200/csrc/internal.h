@@ -158,7 +158,9 @@ struct DiffBwdPlan {
 };
 struct DiffBwdScratch {
   void* da;      // [B, N, D] in dtype
-  float* stats;  // [B*H][tiles of 64 queries][5][64]: -lse_m log2 e, -delta_m, -lambda
+  // [B*H][tiles of 64 queries][5][64]: -lse_1 log2 e, -lse_2 log2 e + log2 lambda,
+  // -delta_m, -1; with lambda given as a value the second without it, the last -lambda
+  float* stats;
   float* dlam;   // [B*H][N]: dlambda per token, where one lambda is shared by all
 };
 DiffBwdPlan diff_bwd_plan(int B, int N, int H, int d, sva_dtype_t dt);

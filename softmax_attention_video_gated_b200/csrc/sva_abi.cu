@@ -342,7 +342,6 @@ extern "C" sva_status_t sva_diff_anchor_bwd(const sva_diff_args* args, const sva
                                                      args->n_keys, args->dtype))
     return SVA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = clear_status(ws, s)) != SVA_OK) return st;
   void* scratch = static_cast<char*>(ws) + SVA_STATUS_BYTES;
   const cudaError_t e = diff_bwd(*args, *grads, static_cast<int*>(ws), scratch, s);
   return e == cudaSuccess ? SVA_OK : cuda_fail(e);
