@@ -53,13 +53,20 @@ struct Sum {
 #pragma unroll
     for (int i = 0; i < 4; ++i) big[i] = small[i] = 0.f;
   }
-  __device__ __forceinline__ void add(const FragA& a, const FragB& b) {
-    mma(small, a.lo, b.hi);
-    mma(small, a.hi, b.lo);
-    mma(big, a.hi, b.hi);
-  }
   __device__ __forceinline__ float at(int i) const { return big[i] + small[i]; }
 };
+
+// x += a b and y += c d, their MMAs in turn: one that adds to the same sum follows
+// three others, about its latency
+__device__ __forceinline__ void add2(Sum& x, const FragA& a, const FragB& b, Sum& y, const FragA& c,
+                                     const FragB& d) {
+  mma(x.small, a.lo, b.hi);
+  mma(y.small, c.lo, d.hi);
+  mma(x.big, a.hi, b.hi);
+  mma(y.big, c.hi, d.hi);
+  mma(x.small, a.hi, b.lo);
+  mma(y.small, c.hi, d.lo);
+}
 
 // A lane's place in a 16 x 8 tile: rows g and g + 8; as a result the columns 2 t and
 // 2 t + 1, as a left operand the summed indexes t and t + 4.
@@ -156,8 +163,7 @@ __device__ __forceinline__ void scores(float (&s)[2][4], const uint32_t* hi, con
     frag_a<L>(a, hi, lo, r, k0 + k, ln);
     frag_dot<L>(b[0], y, c, k0 + k, ln);
     frag_dot<L>(b[1], y, c + 8, k0 + k, ln);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) acc[n].add(a, b[n]);
+    add2(acc[0], a, b[0], acc[1], a, b[1]);
   }
 #pragma unroll
   for (int n = 0; n < 2; ++n)
@@ -269,15 +275,15 @@ __global__ void __launch_bounds__(128, 2)
         FragB v[2];
         frag_rows<L>(v[0], vs, c, n * 8, ln);
         frag_rows<L>(v[1], vs, c + 8, n * 8, ln);
+        Sum acc[2];
+        acc[0].clear();
+        acc[1].clear();
+        add2(acc[0], p[0][0], v[0], acc[1], p[1][0], v[0]);
+        add2(acc[0], p[0][1], v[1], acc[1], p[1][1], v[1]);
 #pragma unroll
-        for (int mp = 0; mp < 2; ++mp) {
-          Sum acc;
-          acc.clear();
-          acc.add(p[mp][0], v[0]);
-          acc.add(p[mp][1], v[1]);
+        for (int mp = 0; mp < 2; ++mp)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[mp][n][i] += acc.at(i);
-        }
+          for (int i = 0; i < 4; ++i) o[mp][n][i] += acc[mp].at(i);
       }
     }
   }
@@ -344,16 +350,21 @@ template <int NT, int L>
 __device__ __forceinline__ void mix(float (&acc)[NT][4], const FragA (&w)[2], const float* x, int c,
                                     int n0, Lane ln) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    FragB v[2];
-    frag_rows<L>(v[0], x, c, n0 + n * 8, ln);
-    frag_rows<L>(v[1], x, c + 8, n0 + n * 8, ln);
-    Sum s;
-    s.clear();
-    s.add(w[0], v[0]);
-    s.add(w[1], v[1]);
+  for (int n = 0; n < NT; n += 2) {
+    Sum s[2];
+    s[0].clear();
+    s[1].clear();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] += s.at(i);
+    for (int k = 0; k < 2; ++k) {
+      FragB v[2];
+      frag_rows<L>(v[0], x, c + 8 * k, n0 + n * 8, ln);
+      frag_rows<L>(v[1], x, c + 8 * k, n0 + n * 8 + 8, ln);
+      add2(s[0], w[k], v[0], s[1], w[k], v[1]);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n + j][i] += s[j].at(i);
   }
 }
 
