@@ -170,6 +170,34 @@ def test_no_upstream_gradient_and_aliases():
     assert_close(to_host(dh), zero["dh"], "f32", "dh without dh_out")
 
 
+def test_offsets_past_32_bits():
+    # a tensor of more than 2^31 values, zero but for its last rows: those rows, and the sums over all
+    N, D, last = 300_000, 8192, 40
+    assert (N - last) * D > 2 ** 31
+    torch.manual_seed(5)
+    h = torch.zeros(1, N, D, device="cuda")
+    o = torch.zeros(1, N, D, device="cuda", dtype=torch.bfloat16)
+    h[:, -last:].normal_()
+    o[:, -last:].normal_()
+    h_tail, o_tail = to_host(h[:, -last:]), to_host(o[:, -last:])
+    u, stats = torch.empty_like(o), torch.empty(1, N, 4, device="cuda")
+    sva.sva_block_norm_fwd(h, o=o, h_out=h, u=u, stats=stats)
+    du_tail = to_host(u[:, -last:])                       # u, zero but for its last rows, stands for du
+    ref = OD.block_norm(h_tail, o=o_tail, dh_out=np.zeros_like(h_tail), du=du_tail)
+    assert_close(to_host(h[:, -last:]), ref["h_out"], "f32", "h_out")
+    assert_close(du_tail, ref["u"], "bf16", "u")
+    assert not u[:, :-last].any()
+    dh, do, dw = torch.empty_like(h), torch.empty_like(o), torch.empty(D, device="cuda")
+    sva.sva_block_norm_bwd(h, stats, dh, o=o, do=do, du=u, dw_pre=dw)
+    # dh of u itself: u . h'^ is nearly its own length, so dh and do cancel to a share of du and are
+    # held to it; dw_pre is a sum without cancellation
+    for n, got in (("dh", dh), ("do", do)):
+        e = np.abs(to_host(got[:, -last:]) - ref[n]).max()
+        assert e <= 2.0 ** -8 * np.abs(du_tail).max(), (n, e)
+    assert_close(to_host(dw), ref["dw_pre"], "f32", "dw_pre")
+    assert not dh[:, :-last].any()
+
+
 def test_capture_and_two_streams():
     xs = [make(2, 333, 1024, "bf16", 50 + i) for i in range(2)]
     want = [call(x, "bf16", sva.SVA_NORM_LAYER, 1e-6, 0.9) for x in xs]

@@ -91,13 +91,13 @@ def assert_grad(got, x, ref, n, H, dtype):
     assert_close(got, ref[n], dtype, n)
 
 
-def compare(x, t, H, dtype, lens=None, flags=0):
+def compare(x, t, H, dtype, lens=None, flags=0, scale=0.0):
     kl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
-    ref = oracle(x, H, key_lens=lens, raw=bool(flags))
+    ref = oracle(x, H, key_lens=lens, raw=bool(flags), scale=scale or None)
     saved = new_saved(t, H)
-    out, ws = forward(t, H, saved, kl, flags)
+    out, ws = forward(t, H, saved, kl, flags, scale=scale)
     assert sva.sva_check_device_status(ws) == sva.SVA_OK
-    plain, _ = forward(t, H, None, kl, flags)
+    plain, _ = forward(t, H, None, kl, flags, scale=scale)
     assert torch.equal(out, plain)                        # saving changes nothing
     assert_close(to_host(out), ref["out"], dtype, "out")
     for got, n in zip(saved, ("o1", "o2")):
@@ -108,12 +108,12 @@ def compare(x, t, H, dtype, lens=None, flags=0):
     # a sum of exponentials of fp32 dots: 1e-5 of the largest logit at hand
     assert np.abs(lse[fin] - ref["lse"][fin]).max(initial=0.0) <= 1e-5 * max(
         1.0, np.abs(ref["lse"][fin]).max(initial=0.0))
-    g, ws = backward(t, H, saved, kl, flags)
+    g, ws = backward(t, H, saved, kl, flags, scale=scale)
     assert sva.sva_check_device_status(ws) == sva.SVA_OK
     for n in GRADS:
         if g[n] is not None:
             assert_grad(g[n], x, ref, n, H, dtype)
-    again, _ = backward(t, H, saved, kl, flags)
+    again, _ = backward(t, H, saved, kl, flags, scale=scale)
     for n in GRADS:
         assert g[n] is None or torch.equal(g[n], again[n]), n   # no atomics: the same bits
     return ref
@@ -187,11 +187,50 @@ def test_empty_batch_is_zero(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_no_gate(dtype):
-    x = make(1, 100, 90, 2, 128, dtype, 4)
+@pytest.mark.parametrize("N", [1, 3, 100])
+def test_no_gate(dtype, N):
+    x = make(1, N, 90, 2, 128, dtype, 4)
     x["g"] = None
     t = {n: None if v is None else to_dev(v, dtype) for n, v in x.items()}
     compare(x, t, 2, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [2, 70])
+def test_given_scale(dtype, N):
+    x = make(1, N, 130, 2, 128, dtype, 19)
+    compare(x, dev(x, dtype), 2, dtype, scale=0.3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 40])
+def test_offsets_past_32_bits(dtype, N):
+    """Keys and values in rows so far apart that the last ones start behind 2^32 bytes and 2^31
+    elements; all but the last 300 and the first 300 keys are far below in logit."""
+    H, d, Nk = 1, 128, 1100
+    ld = 1 << 21                                       # elements a row
+    torch.manual_seed(3)
+    dt = TDT[dtype]
+    kv = torch.empty(1, Nk, ld, device="cuda", dtype=dt)
+    k, v = kv[..., :d], kv[..., ld - d:]
+    assert (Nk - 1) * ld > 2 ** 31
+    x = make(1, N, Nk, H, d, dtype, 71)
+    t = dev(x, dtype)
+    k.copy_(t["k"])
+    v.copy_(t["v"])
+    out, _ = forward({**t, "k": k, "v": v}, H)
+    saved = new_saved(t, H)
+    near, _ = forward(t, H, saved)
+    assert torch.equal(out, near)
+    if N > 1:  # the gradients' rows as far apart
+        dkv = torch.empty_like(kv)
+        g, _ = backward(t, H, saved)
+        far = {n: torch.empty_like(g[n]) for n in ("dq", "dgate", "dlam")}
+        sva.sva_diff_anchor_bwd(t["q"], k, v, t["g"], t["lam"], t["dout"], saved, far["dq"],
+                                dkv[..., :d], dkv[..., ld - d:], far["dgate"], far["dlam"], H)
+        for n in far:
+            assert torch.equal(far[n], g[n]), n
+        assert torch.equal(dkv[..., :d], g["dk"]) and torch.equal(dkv[..., ld - d:], g["dv"])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
