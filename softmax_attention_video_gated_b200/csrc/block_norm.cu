@@ -198,10 +198,10 @@ struct Group {
   }
 };
 
-// Rows of one launch: every batch is cut into `units` runs of `per` rows, one
-// CTA each; its `groups` groups of W warps take them in turn.
+// Rows of one launch: `units` CTAs of `groups` groups of W warps share a batch, the
+// groups taking its rows in turn.
 struct RowRuns {
-  int W, groups, stages, units, per;
+  int W, groups, stages, units;
   int64_t total;  // B * units
 };
 
@@ -310,8 +310,10 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
   const int h_bytes = width * 4, stage_bytes = h_bytes + (post ? width * static_cast<int>(sizeof(T)) : 0);
   char* ring = reinterpret_cast<char*>(sh + width) + g * rr.stages * stage_bytes;
   const int base = b * a.N;  // rows are numbered over all batches
-  uint32_t t = base + ub * rr.per + g;
-  const uint32_t end = base + static_cast<uint32_t>(min(static_cast<long long>(a.N), (ub + 1LL) * rr.per));
+  // neighbours in time are neighbours in memory: runs of rows of their own, a CTA each,
+  // kept 1,776 streams open at once and 402 MB took 80 us
+  uint32_t t = base + ub * rr.groups + g;
+  const uint32_t end = base + a.N, step = rr.units * rr.groups;
   uint32_t tf = t;
   int sf = 0;  // the next row to fetch and its stage
   auto fetch = [&]() {
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
       if (post) stage_row(st + h_bytes, static_cast<const T*>(a.o) + row * a.ldo, at);
     }
     copy_commit();
-    tf += rr.groups;
+    tf += step;
     sf = sf + 1 == rr.stages ? 0 : sf + 1;
   };
   for (int s = 0; s < rr.stages; ++s) fetch();
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
     SVA_EACH(i) x[i] = x[i] * r;
     return make_float2(mean, r);
   };
-  for (int st = 0; t < end; t += rr.groups) {
+  for (int st = 0; t < end; t += step) {
     const int64_t row = t;
     float4 h[NQ], x[NQ];
     copy_wait(rr.stages);
@@ -417,8 +419,8 @@ __global__ void __launch_bounds__(MAXT)
   const int64_t ldhs = post ? a.ldho : a.ldh;
   const float* hsrc = post ? a.h_out : a.h;
   const int base = b * a.N;  // rows are numbered over all batches; addresses are made of the
-  uint32_t t = base + ub * rr.per + g;  // number each time, which costs less than six pointers kept
-  const uint32_t end = base + static_cast<uint32_t>(min(static_cast<long long>(a.N), (ub + 1LL) * rr.per));
+  uint32_t t = base + ub * rr.groups + g;  // number each time, which costs less than six pointers kept
+  const uint32_t end = base + a.N, step = rr.units * rr.groups;
   uint32_t tf = t;
   int sf = 0;
   auto fetch = [&]() {
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(MAXT)
       if (post) stage_row(st + at_o, static_cast<const T*>(a.o) + row * a.ldo, at);
     }
     copy_commit();
-    tf += rr.groups;
+    tf += step;
     sf = sf + 1 == rr.stages ? 0 : sf + 1;
   };
   for (int s = 0; s < rr.stages; ++s) fetch();
@@ -443,10 +445,10 @@ __global__ void __launch_bounds__(MAXT)
   SVA_EACH(i) sum_du[i] = sum_dux[i] = sum_do[i] = all4(0.f);
   const float4* stats = reinterpret_cast<const float4*>(a.stats);
   float4 st_next = t < end ? stats[t] : all4(0.f);
-  for (int st = 0; t < end; t += rr.groups) {
+  for (int st = 0; t < end; t += step) {
     const int64_t row = t;
     const float4 st4 = st_next;
-    if (t + rr.groups < end) st_next = stats[t + rr.groups];
+    if (t + step < end) st_next = stats[t + step];
     float4 dh[NQ], y[NQ];
     copy_wait(rr.stages);
     __syncwarp();
@@ -650,20 +652,20 @@ RowRuns row_runs(int B, int N, int D, int cta_warps, int warps, int factors, int
   while (per_sm > 1 && 2 * stage > room(per_sm)) --per_sm;
   r.stages = std::max(1, std::min(kMaxStages, room(per_sm) / stage));
   const int64_t slots = static_cast<int64_t>(std::max(1, device_sm_count())) * per_sm;
-  int64_t best = INT64_MAX;
+  int64_t best = INT64_MAX, rows = 1;
   for (int64_t w = 1; w <= 4; ++w) {
-    const int64_t u = std::max<int64_t>(1, std::min<int64_t>((N + r.groups - 1) / r.groups, w * slots / B));
-    const int64_t per = (N + u - 1) / u, rows = (per + r.groups - 1) / r.groups;
-    const int64_t units = (N + per - 1) / per;
-    const int64_t cost = (units * B + slots - 1) / slots * (rows + 2);
+    const int64_t most = (static_cast<int64_t>(N) + r.groups - 1) / r.groups;
+    const int64_t u = std::max<int64_t>(1, std::min(most, w * slots / B));
+    const int64_t per_group = (most + u - 1) / u;
+    const int64_t cost = (u * B + slots - 1) / slots * (per_group + 2);
     if (cost < best) {
       best = cost;
-      r.per = static_cast<int>(per);
-      r.units = static_cast<int>(units);
+      rows = per_group;
+      r.units = static_cast<int>(u);
     }
   }
   r.total = static_cast<int64_t>(B) * r.units;
-  r.stages = std::min(r.stages, (r.per + r.groups - 1) / r.groups);
+  r.stages = static_cast<int>(std::min<int64_t>(r.stages, rows));
   return r;
 }
 
