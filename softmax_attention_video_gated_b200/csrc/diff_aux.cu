@@ -198,8 +198,9 @@ DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt) {
   const int64_t slots = static_cast<int64_t>(std::max(1, device_sm_count())) * (tc ? 1 : 2);
   p.n_full = static_cast<int>(units);
   // The last wave's units, cut s ways, take waves(s) x (their key blocks + 2
-  // blocks' time for a CTA's start and end), and one more such time for the
-  // merge. Cut them where that saves a fifth of the wave at least.
+  // blocks' time for a CTA's start and end), and two more such times for writing
+  // the parts and for the merge. Cut them where that saves a fifth of the wave at
+  // least.
   const int64_t tail = units % slots;
   int64_t best = nkb + 2;
   const int64_t most = best * 4 / 5;
@@ -209,6 +210,23 @@ DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt) {
       best = cost;
       p.split = static_cast<int>(sp);
     }
+  }
+  // fp32, nothing but that wave: parts that are all resident at once can be a cluster and
+  // join in it, in one block's time (1,024 tokens, 4 heads of 64: 47 us and 11 for the
+  // merge -> 52; clusters that wait for a second wave lose more than the merge costs).
+  // Clusters of eight leave some SMs of a GPC over.
+  for (int64_t sp = 2; !tc && units < slots && sp <= std::min<int64_t>(nkb, 8); sp *= 2) {
+    const int64_t cost = (nkb + sp - 1) / sp + 2 + 1;
+    if (units * sp <= (sp == 8 ? slots * 7 / 8 : slots) && cost < best && cost <= most) {
+      best = cost;
+      p.split = static_cast<int>(sp);
+      p.cluster = true;
+    }
+  }
+  if (p.cluster) {
+    p.n_full = 0;
+    p.n_split_units = static_cast<int>(units);
+    return p;
   }
   if (p.split > 1) {
     p.n_split_units = static_cast<int>(tail);
@@ -220,7 +238,7 @@ DiffPlan diff_plan(int B, int N, int H, int d, int n_keys, sva_dtype_t dt) {
 }
 
 cudaError_t diff_merge(const sva_diff_args& a, const DiffPlan& p, void* scratch, cudaStream_t s) {
-  if (p.n_split_units == 0) return cudaSuccess;
+  if (p.n_split_units == 0 || p.cluster) return cudaSuccess;
   const DiffWork wk = diff_work(p, a.H, scratch);
   const int64_t threads = static_cast<int64_t>(p.n_split_units) * p.rows * 32;
   const unsigned grid = static_cast<unsigned>((threads + 255) / 256);

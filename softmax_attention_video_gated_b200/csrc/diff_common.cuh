@@ -140,10 +140,11 @@ inline bool diff_map(CUtensorMap* m, const void* base, int64_t ld, int B, int N,
 // unnormalised output and (running maximum in log2 units, sum) per row.
 struct DiffWork {
   int n_qtiles, H, rows, n_full, split;
+  bool cluster;    // a unit's parts are a cluster and join there
   float* partial;  // [unit][part][map][rows x d O | rows x (m, l)]
 };
 __host__ __device__ inline DiffWork diff_work(const DiffPlan& p, int H, void* scratch) {
-  return {p.n_qtiles, H, p.rows, p.n_full, p.split, static_cast<float*>(scratch)};
+  return {p.n_qtiles, H, p.rows, p.n_full, p.split, p.cluster, static_cast<float*>(scratch)};
 }
 struct DiffUnit {
   int q0, h, b, part, su;  // part < 0: the unit runs whole
@@ -172,6 +173,56 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+
+// The end of a unit whose key parts are the CTAs of one cluster: every CTA has its part's
+// outputs (unnormalised) in os [2 maps][ROWS][L] and (maximum, sum) in mls [2][ROWS][2], and
+// joins a share of the rows, reading the others' over distributed shared memory in the order
+// of the parts. w: room for 2 * ROWS * (8 + 1) floats. All threads of the CTA, which must
+// have written os and mls before.
+template <typename T, int ROWS, int D, int L>
+__device__ __forceinline__ void cluster_finish(const sva_diff_args& a, const DiffUnit& u, int split,
+                                               const float* os, const float* mls, float* w) {
+  cluster_sync();
+  const int r0 = ROWS * u.part / split, rows = ROWS * (u.part + 1) / split - r0;
+  for (int i = threadIdx.x; i < 2 * rows; i += blockDim.x) {
+    const int mp = i / rows, r = r0 + i % rows;
+    float2 ml[8];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      ml[p] = make_float2(-INFINITY, 0.f);
+      if (p < split) ml[p] = ld_cluster2(mls + 2 * (mp * ROWS + r), static_cast<uint32_t>(p));
+      mx = fmaxf(mx, ml[p].x);
+    }
+    float l = 0.f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      // a part without keys has a weight of zero, and its outputs are zero
+      const float wp = ml[p].x == -INFINITY ? 0.f : exp2f(ml[p].x - mx);
+      l = fmaf(wp, ml[p].y, l);
+      w[(mp * ROWS + r) * 9 + p] = wp;
+    }
+    w[(mp * ROWS + r) * 9 + 8] = l;
+    const int t = u.q0 + r;
+    if (t < a.N) finish_lse(a, mp, u.b, u.h, t, mx, l);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * D / 4; i += blockDim.x) {
+    const int r = r0 + i / (D / 4), c = (i % (D / 4)) * 4, t = u.q0 + r;
+    if (t >= a.N) break;
+    const float *w1 = w + r * 9, *w2 = w + (ROWS + r) * 9;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+    for (int p = 0; p < split; ++p) {
+      const float4 o1 = ld_cluster4(os + r * L + c, static_cast<uint32_t>(p));
+      const float4 o2 = ld_cluster4(os + (ROWS + r) * L + c, static_cast<uint32_t>(p));
+      x = make_float4(fmaf(w1[p], o1.x, x.x), fmaf(w1[p], o1.y, x.y), fmaf(w1[p], o1.z, x.z), fmaf(w1[p], o1.w, x.w));
+      y = make_float4(fmaf(w2[p], o2.x, y.x), fmaf(w2[p], o2.y, y.y), fmaf(w2[p], o2.z, y.z), fmaf(w2[p], o2.w, y.w));
+    }
+    finish4<T>(a, u.b, u.h, t, c, x, y, w1[8], w2[8], lambda_of<T>(a, u.b, t, u.h));
+  }
+  cluster_sync();  // nobody leaves while its shared memory is read
 }
 
 }  // namespace

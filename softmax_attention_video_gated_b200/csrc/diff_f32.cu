@@ -179,6 +179,7 @@ __device__ __forceinline__ void scores(float (&s)[2][4], const uint32_t* hi, con
 // ---------------------------------------------------------------------------
 
 constexpr int FR = kDiffF32Rows;  // 4 warps
+static_assert(4 * FR + 2 * FR * 9 <= 4 * 16 * (64 + 4), "sums and weights fit the tiles' place");
 
 template <int D>
 constexpr size_t fwd_smem() {
@@ -310,6 +311,10 @@ __global__ void __launch_bounds__(128, 2)
       for (int i = 0; i < 2; ++i)
         *reinterpret_cast<float2*>(mls + 2 * (mp * FR + r + ln.g + 8 * i)) =
             make_float2(m[mp][i], l[mp][i]);
+  if (wk.cluster) {
+    cluster_finish<float, FR, D, L>(a, u, wk.split, os, mls, mls + 4 * FR);
+    return;
+  }
   __syncwarp();  // a warp's rows are its own
   const int lane = lane_id();
   for (int i = lane; i < 16 * D / 4; i += 32) {
@@ -554,8 +559,9 @@ cudaError_t fwd(const sva_diff_args& a, void* scratch, cudaStream_t s) {
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
   cudaError_t e = allow_max_smem<diff_fwd_kernel<D>>();
   if (e != cudaSuccess) return e;
-  diff_fwd_kernel<D><<<p.grid(), 128, fwd_smem<D>(), s>>>(a, scale * kLog2e, diff_work(p, a.H, scratch));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_clusters(diff_fwd_kernel<D>, p.grid(), 128, fwd_smem<D>(), p.cluster ? p.split : 1, s, a,
+                      scale * kLog2e, diff_work(p, a.H, scratch));
+  if (e != cudaSuccess) return e;
   return diff_merge(a, p, scratch, s);
 }
 

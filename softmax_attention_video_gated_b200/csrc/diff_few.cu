@@ -21,12 +21,6 @@ namespace {
 
 constexpr int WARPS = 8;
 
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_map(p, rank)) : "memory");
-  return v;
-}
-
 template <typename T>
 __device__ __forceinline__ void widen16(uint4 x, float (&f)[16 / sizeof(T)]);
 template <>
@@ -232,18 +226,8 @@ cudaError_t launch(const sva_diff_args& a, int* status, cudaStream_t s) {
   int cluster = 1;  // two steps of every subgroup at least
   while (cluster < 8 && Nk > cluster * SUBS * few_unroll(R) * 2) cluster *= 2;
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.H * cluster));
-  cfg.blockDim = dim3(32 * WARPS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, diff_few_kernel<T, D, R>, a, scale * kLog2e, cluster, status);
+  return launch_clusters(diff_few_kernel<T, D, R>, static_cast<unsigned>(a.B * a.H * cluster), 32 * WARPS,
+                         smem, cluster, s, a, scale * kLog2e, cluster, status);
 }
 
 template <typename T, int D>

@@ -71,6 +71,24 @@ cudaError_t allow_max_smem() {
   return e;
 }
 
+// One launch with clusters of `cluster` CTAs (1: without).
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem, int cluster,
+                            cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 constexpr size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- projections
@@ -140,6 +158,7 @@ constexpr int diff_f32_keys(int d) { return d > 64 ? 16 : 32; }  // two stages o
 // wave may be cut `split` ways along the keys, with parts in scratch.
 struct DiffPlan {
   int rows = 0, n_qtiles = 0, n_full = 0, n_split_units = 0, split = 1;
+  bool cluster = false;  // every unit is split, its parts are a cluster and join there: no scratch
   size_t partial_bytes = 0;
   unsigned grid() const { return static_cast<unsigned>(n_full + n_split_units * split); }
 };
