@@ -272,6 +272,7 @@ cudaError_t diff_bwd(const sva_diff_args& a, const sva_diff_grads& g, int* statu
   const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
   const cudaError_t e = tc ? prepare<__nv_bfloat16>(a, g, ws, status, s) : prepare<float>(a, g, ws, status, s);
   if (e != cudaSuccess) return e;
+  if (a.N <= kDiffFewRows) return diff_bwd_few(a, g, scratch, s);
   return tc ? diff_bwd_bf16(a, g, status, scratch, s) : diff_bwd_f32(a, g, scratch, s);
 }
 

@@ -186,6 +186,7 @@ DiffBwdPlan diff_bwd_plan(int B, int N, int H, int d, sva_dtype_t dt);
 DiffBwdScratch diff_bwd_scratch(const sva_diff_args& a, void* scratch);
 cudaError_t diff_bwd(const sva_diff_args& a, const sva_diff_grads& g, int* status, void* scratch,
                      cudaStream_t s);
+cudaError_t diff_bwd_few(const sva_diff_args& a, const sva_diff_grads& g, void* scratch, cudaStream_t s);
 cudaError_t diff_bwd_f32(const sva_diff_args& a, const sva_diff_grads& g, void* scratch,
                          cudaStream_t s);
 cudaError_t diff_bwd_bf16(const sva_diff_args& a, const sva_diff_grads& g, int* status,
