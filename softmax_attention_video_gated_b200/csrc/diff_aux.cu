@@ -259,6 +259,21 @@ DiffBwdPlan diff_bwd_plan(int B, int N, int H, int d, sva_dtype_t dt) {
   return p;
 }
 
+DiffBwdGrid diff_bwd_grid(const sva_diff_args& a, int rows, int streamed, int ctas_per_sm) {
+  const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
+  const int key_tiles = (Nk + rows - 1) / rows, query_tiles = (a.N + rows - 1) / rows;
+  DiffBwdGrid r;
+  r.keys_first = a.N >= Nk;
+  r.first = r.keys_first ? key_tiles : query_tiles;
+  r.second = r.keys_first ? query_tiles : key_tiles;
+  // four blocks a cut at least
+  const int64_t blocks = (std::max(a.N, Nk) + streamed - 1) / streamed;
+  const int64_t ctas = static_cast<int64_t>(r.first) * a.B * a.H;
+  const int64_t slots = static_cast<int64_t>(std::max(1, device_sm_count())) * ctas_per_sm;
+  while (r.cuts < 8 && ctas * r.cuts * 2 <= slots && blocks >= 8 * r.cuts) r.cuts *= 2;
+  return r;
+}
+
 DiffBwdScratch diff_bwd_scratch(const sva_diff_args& a, void* scratch) {
   const DiffBwdPlan p = diff_bwd_plan(a.B, a.N, a.H, a.d, a.dtype);
   char* base = static_cast<char*>(scratch);

@@ -98,20 +98,25 @@ struct Maps {  // boxes of 128 standing rows of K and V; of 64 streamed rows of 
 
 template <bool KV>
 __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& a,
-                                         const sva_diff_grads& g, const DiffBwdScratch& ws, int tile,
-                                         int bh, float scale, int* status, uint8_t* smem_raw) {
+                                         const sva_diff_grads& g, const DiffBwdScratch& ws,
+                                         const DiffBwdTile& u, float scale, int* status,
+                                         uint8_t* smem_raw) {
   const CUtensorMap &map_x = maps.k_stand, &map_y = maps.v_stand;  // Q and dA stand in TMEM, loaded by threads
   const CUtensorMap &map_x2 = KV ? maps.q : maps.k, &map_y2 = KV ? maps.da : maps.v;
   using L = Layout<KV>;
+  constexpr int NC = KV ? 2 * HD : HD;  // columns of the results
+  static_assert(BR * (NC + 4) * 4 <= L::TAIL - L::RING, "a share fits the ring's place");
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   Tail* tl = reinterpret_cast<Tail*>(smem + L::TAIL);
-  const int h = bh % a.H, b = bh / a.H;
+  const int bh = u.bh, h = bh % a.H, b = bh / a.H;
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const int valid = key_count(a.key_lens, b, Nk);
-  const int r0 = tile * BR;
+  const int r0 = u.tile * BR;
   const int n_stat_tiles = (a.N + 63) / 64;
-  const int n = KV ? (r0 < valid ? n_stat_tiles : 0) : (valid + BS - 1) / BS;
+  // this CTA's blocks of the streamed side: [j0, j0 + n)
+  const int n_all = KV ? (r0 < valid ? n_stat_tiles : 0) : (valid + BS - 1) / BS;
+  const int j0 = u.cut * n_all / u.cuts, n = (u.cut + 1) * n_all / u.cuts - j0;
   const float scale_log2 = scale * kLog2e;
   const int warp = warp_uniform(warp_id()), lane = lane_id();
   const int wg = warp >> 2;
@@ -168,12 +173,12 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
         if (lane == 0) {
           uint8_t* p = smem + L::RING + st * STAGE_BYTES;
           mbar_arrive_expect_tx(&tl->full[st], STAGE_BYTES + (KV ? STAT_BYTES : 0));
-          tma_load_3d(&map_x2, &tl->full[st], p, h * HD, j * BS, b);
-          tma_load_3d(&map_x2, &tl->full[st], p + BOXS, h * HD + 64, j * BS, b);
-          tma_load_3d(&map_y2, &tl->full[st], p + 2 * BOXS, h * HD, j * BS, b);
-          tma_load_3d(&map_y2, &tl->full[st], p + 3 * BOXS, h * HD + 64, j * BS, b);
+          tma_load_3d(&map_x2, &tl->full[st], p, h * HD, (j0 + j) * BS, b);
+          tma_load_3d(&map_x2, &tl->full[st], p + BOXS, h * HD + 64, (j0 + j) * BS, b);
+          tma_load_3d(&map_y2, &tl->full[st], p + 2 * BOXS, h * HD, (j0 + j) * BS, b);
+          tma_load_3d(&map_y2, &tl->full[st], p + 3 * BOXS, h * HD + 64, (j0 + j) * BS, b);
           if (KV)
-            bulk_load(smem + L::STAT + st * STAT_BYTES, ws.stats + stat_at(bh, n_stat_tiles, j * BS),
+            bulk_load(smem + L::STAT + st * STAT_BYTES, ws.stats + stat_at(bh, n_stat_tiles, (j0 + j) * BS),
                       STAT_BYTES, &tl->full[st]);
         }
         __syncwarp();
@@ -223,7 +228,7 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
         if (!__all_sync(0xffffffffu, mbar_wait(&tl->full[st], (j / STAGES) & 1, abort_flag, status,
                                                WHERE_DIFF_BWD)))
           return false;
-        const int left = valid - j * BS;
+        const int left = valid - (j0 + j) * BS;
         if (!KV && left < BS && valid < Nk) {
           uint8_t* p = smem + L::RING + st * STAGE_BYTES;
           for (int i = left * 8 + lane; i < BS * 8; i += 32) {
@@ -385,7 +390,7 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
           d2[k] = pack_bf16x2(y0, y1);
         }
         if (!KV) {  // keys of block i - 1 that count
-          const int left = valid - (i - 1) * BS - COLS * part;
+          const int left = valid - (j0 + i - 1) * BS - COLS * part;
           if (left < COLS) {
 #pragma unroll
             for (int k = 0; k < COLS / 2; ++k) {
@@ -489,6 +494,16 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
         tmem_ld32(lane_base + col0 + c, o);
         tmem_wait_ld();
       }
+      if (u.cuts > 1) {  // a share of the sum: in fp32 to shared memory, the ring's place
+        float* os = reinterpret_cast<float*>(smem + L::RING) + r * (NC + 4) + ncols * part + c;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4*>(os + 4 * k) =
+              zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : make_float4(f * __uint_as_float(o[4 * k]), f * __uint_as_float(o[4 * k + 1]),
+                                 f * __uint_as_float(o[4 * k + 2]), f * __uint_as_float(o[4 * k + 3]));
+        continue;
+      }
       if (row >= n_rows) continue;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -510,23 +525,43 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
+  if (u.cuts > 1) {
+    // the cuts of a tile are a cluster; the first adds up the shares, in their order
+    cluster_sync();
+    if (u.cut == 0) {
+      const int n_rows = KV ? Nk : a.N;
+      const float* os = reinterpret_cast<const float*>(smem + L::RING);
+      for (int i = threadIdx.x; i < BR * NC / 4; i += NUM_THREADS) {
+        const int r = i / (NC / 4), c = (i % (NC / 4)) * 4, row = r0 + r;
+        if (row >= n_rows) break;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < u.cuts; ++p) {
+          const float4 y = ld_cluster4(os + r * (NC + 4) + c, static_cast<uint32_t>(p));
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        const int64_t at = static_cast<int64_t>(b) * n_rows + row;
+        __nv_bfloat16* dst = !KV      ? static_cast<__nv_bfloat16*>(g.dq) + at * g.lddq
+                             : c < HD ? static_cast<__nv_bfloat16*>(g.dk) + at * g.lddk
+                                      : static_cast<__nv_bfloat16*>(g.dv) + at * g.lddv;
+        store4(dst + h * HD + c % HD, x);
+      }
+    }
+    cluster_sync();  // nobody leaves while its shared memory is read
+  }
 }
 
-// Both sides in one launch, the longer tiles (keys stand) first: the second fills the
-// first's last wave.
+// Both sides in one launch, the second filling the first's last wave.
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     diff_bwd_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ sva_diff_args a,
-                       const __grid_constant__ sva_diff_grads g, DiffBwdScratch ws, int key_tiles,
-                       int query_tiles, float scale, int* status) {
+                       const __grid_constant__ sva_diff_grads g, DiffBwdScratch ws, DiffBwdGrid grid,
+                       float scale, int* status) {
   extern __shared__ uint8_t smem_raw[];
-  int cta = static_cast<int>(blockIdx.x);
-  const int n_key = key_tiles * a.B * a.H;
-  if (cta < n_key) {
-    bwd_tile<true>(maps, a, g, ws, cta % key_tiles, cta / key_tiles, scale, status, smem_raw);
-  } else {
-    cta -= n_key;
-    bwd_tile<false>(maps, a, g, ws, cta % query_tiles, cta / query_tiles, scale, status, smem_raw);
-  }
+  DiffBwdTile u;
+  if (!diff_bwd_tile(grid, a.B * a.H, static_cast<int>(blockIdx.x), u)) return;
+  if (u.keys_stand)
+    bwd_tile<true>(maps, a, g, ws, u, scale, status, smem_raw);
+  else
+    bwd_tile<false>(maps, a, g, ws, u, scale, status, smem_raw);
 }
 
 }  // namespace
@@ -545,11 +580,10 @@ cudaError_t diff_bwd_bf16(const sva_diff_args& a, const sva_diff_grads& g, int* 
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_max_smem<diff_bwd_tc_kernel>();
   if (e != cudaSuccess) return e;
-  const int key_tiles = (Nk + BR - 1) / BR, query_tiles = (a.N + BR - 1) / BR;
+  const DiffBwdGrid grid = diff_bwd_grid(a, BR, BS, 1);
   constexpr size_t smem = Layout<true>::SMEM > Layout<false>::SMEM ? Layout<true>::SMEM : Layout<false>::SMEM;
-  diff_bwd_tc_kernel<<<static_cast<unsigned>((key_tiles + query_tiles) * a.B * a.H), NUM_THREADS, smem, s>>>(
-      m, a, g, ws, key_tiles, query_tiles, scale, status);
-  return cudaGetLastError();
+  return launch_clusters(diff_bwd_tc_kernel, grid.ctas(a.B * a.H), NUM_THREADS, smem, grid.cuts, s, m, a, g, ws,
+                         grid, scale, status);
 }
 
 }  // namespace sva

@@ -175,6 +175,25 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// A backward CTA's tile: cut `cut` of `cuts` of its stream.
+struct DiffBwdTile {
+  int tile, bh, cut, cuts;
+  bool keys_stand;
+};
+// false: the CTA only fills up a cluster
+__device__ __forceinline__ bool diff_bwd_tile(const DiffBwdGrid& grid, int heads, int cta, DiffBwdTile& u) {
+  const int n_first = grid.first * heads * grid.cuts;
+  const bool in_first = cta < n_first;
+  u.keys_stand = in_first == grid.keys_first;
+  u.cuts = in_first ? grid.cuts : 1;
+  u.cut = in_first ? cta % grid.cuts : 0;
+  const int unit = in_first ? cta / grid.cuts : cta - n_first;
+  const int tiles = in_first ? grid.first : grid.second;
+  u.tile = unit % tiles;
+  u.bh = unit / tiles;
+  return u.bh < heads;
+}
+
 // The end of a unit whose key parts are the CTAs of one cluster: every CTA has its part's
 // outputs (unnormalised) in os [2 maps][ROWS][L] and (maximum, sum) in mls [2][ROWS][2], and
 // joins a share of the rows, reading the others' over distributed shared memory in the order

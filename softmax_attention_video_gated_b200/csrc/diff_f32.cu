@@ -380,7 +380,7 @@ __device__ __forceinline__ void mix(float (&acc)[NT][4], const FragA (&w)[2], co
 // KV = true: key rows stand (X = K, Y = V), queries stream (X' = Q, Y' = dA), out dK, dV.
 template <int D, bool KV>
 __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_grads& g,
-                                         const DiffBwdScratch& ws, float scale, int tile, int bh,
+                                         const DiffBwdScratch& ws, float scale, const DiffBwdTile& u,
                                          float* sm) {
   constexpr int M = D / 2, L = D + 4, NT = D / 8;
   uint32_t* xhi = reinterpret_cast<uint32_t*>(sm);
@@ -391,10 +391,10 @@ __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_
   float* stats = ring + 4 * BS * L;                 // and, KV, of the queries' statistics [5][64]
   const Lane ln;
   const int r = (warp_id() & 1) * 16, quarter = warp_id() >> 1;
-  const int h = bh % a.H, b = bh / a.H;
+  const int bh = u.bh, h = bh % a.H, b = bh / a.H;
   const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   const int valid = key_count(a.key_lens, b, Nk);
-  const int r0 = tile * BR;
+  const int r0 = u.tile * BR;
   const float scale_log2 = scale * kLog2e;
   const int64_t D_all = static_cast<int64_t>(a.H) * D;
   const int n_stat_tiles = (a.N + 63) / 64;
@@ -411,7 +411,10 @@ __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_
       for (int k = 0; k < kStats; ++k)
         rs[i][k] = ws.stats[stat_at(bh, n_stat_tiles, r0 + r + ln.g + 8 * i) + 64 * k];
   }
-  const int stream = KV ? (r0 < valid ? a.N : 0) : valid;
+  // this CTA's rows of the streamed side: [first, stream)
+  const int all = KV ? (r0 < valid ? a.N : 0) : valid, blocks = (all + BS - 1) / BS;
+  const int first = u.cut * blocks / u.cuts * BS;
+  const int stream = min(all, (u.cut + 1) * blocks / u.cuts * BS);
   float acc[NT][4];             // dQ or dK
   float accv[KV ? NT : 1][4];   // dV
 #pragma unroll
@@ -436,8 +439,8 @@ __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_
       load_rows<BS, D>(y2, a.v, a.ldv, b, Nk, h * D, s0, valid);
     }
   };
-  fetch(0);
-  for (int s0 = 0; s0 < stream; s0 += BS) {
+  fetch(first);
+  for (int s0 = first; s0 < stream; s0 += BS) {
     copy_wait_all();
     __syncthreads();  // the block is here, and nobody reads the other stage any more
     fetch(s0 + BS);
@@ -515,6 +518,34 @@ __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_
     }
     __syncthreads();
   }
+  if (u.cuts > 1) {
+    // the cuts of a tile are a cluster; the first adds up their sums, in their order
+    if (quarter == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        js[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        if constexpr (KV)
+          js[(NT + n) * 32] = make_float4(accv[n][0], accv[n][1], accv[n][2], accv[n][3]);
+      }
+    }
+    cluster_sync();
+    if (u.cut == 0 && quarter == 0) {
+      for (int p = 1; p < u.cuts; ++p) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float4 j = ld_cluster4(reinterpret_cast<const float*>(js + n * 32), static_cast<uint32_t>(p));
+          acc[n][0] += j.x; acc[n][1] += j.y; acc[n][2] += j.z; acc[n][3] += j.w;
+          if constexpr (KV) {
+            const float4 jv =
+                ld_cluster4(reinterpret_cast<const float*>(js + (NT + n) * 32), static_cast<uint32_t>(p));
+            accv[n][0] += jv.x; accv[n][1] += jv.y; accv[n][2] += jv.z; accv[n][3] += jv.w;
+          }
+        }
+      }
+    }
+    cluster_sync();  // nobody leaves while its shared memory is read
+    if (u.cut != 0) return;
+  }
   if (quarter != 0) return;
   const int n_rows = KV ? Nk : a.N;
 #pragma unroll
@@ -539,18 +570,18 @@ __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_
   }
 }
 
-// Both sides in one launch, the longer tiles (keys stand) first.
+// Both sides in one launch, the second filling the first's last wave.
 template <int D>
 __global__ void __launch_bounds__(256)
     diff_bwd_kernel(const __grid_constant__ sva_diff_args a, const __grid_constant__ sva_diff_grads g,
-                    DiffBwdScratch ws, float scale, int key_tiles) {
+                    DiffBwdScratch ws, float scale, DiffBwdGrid grid) {
   extern __shared__ __align__(16) float sm[];
-  const int heads = a.B * a.H;
-  const int tile = static_cast<int>(blockIdx.x) / heads, bh = static_cast<int>(blockIdx.x) % heads;
-  if (tile < key_tiles)
-    bwd_tile<D, true>(a, g, ws, scale, tile, bh, sm);
+  DiffBwdTile u;
+  if (!diff_bwd_tile(grid, a.B * a.H, static_cast<int>(blockIdx.x), u)) return;
+  if (u.keys_stand)
+    bwd_tile<D, true>(a, g, ws, scale, u, sm);
   else
-    bwd_tile<D, false>(a, g, ws, scale, tile - key_tiles, bh, sm);
+    bwd_tile<D, false>(a, g, ws, scale, u, sm);
 }
 
 template <int D>
@@ -569,15 +600,12 @@ template <int D>
 cudaError_t bwd(const sva_diff_args& a, const sva_diff_grads& g, void* scratch, cudaStream_t s) {
   const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf(static_cast<float>(D / 2));
-  const int Nk = a.n_keys > 0 ? a.n_keys : a.N;
   constexpr int smem = static_cast<int>(bwd_smem<D>());
   static_assert(smem <= kMaxSmem, "shared memory of one CTA");
   const cudaError_t e = allow_max_smem<diff_bwd_kernel<D>>();
   if (e != cudaSuccess) return e;
-  const int key_tiles = (Nk + BR - 1) / BR, query_tiles = (a.N + BR - 1) / BR;
-  diff_bwd_kernel<D><<<static_cast<unsigned>((key_tiles + query_tiles) * a.B * a.H), 256, smem, s>>>(
-      a, g, ws, scale, key_tiles);
-  return cudaGetLastError();
+  const DiffBwdGrid grid = diff_bwd_grid(a, BR, BS, 1);
+  return launch_clusters(diff_bwd_kernel<D>, grid.ctas(a.B * a.H), 256, smem, grid.cuts, s, a, g, ws, scale, grid);
 }
 
 }  // namespace

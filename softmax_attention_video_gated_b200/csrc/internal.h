@@ -182,6 +182,18 @@ struct DiffBwdScratch {
   float* stats;
   float* dlam;   // [B*H][N]: dlambda per token, where one lambda is shared by all
 };
+// One launch of the backward tiles: `first` tiles a (batch, head) of the side whose
+// tiles take longer (their streamed side is the longer one), each cut `cuts` ways along
+// that stream where there are too few of them, the cuts being a cluster; then the
+// other side's tiles.
+struct DiffBwdGrid {
+  int first = 0, second = 0, cuts = 1;
+  bool keys_first = true;  // the first side's tiles are keys (dK, dV), else queries (dQ)
+  unsigned ctas(int heads) const {
+    return static_cast<unsigned>((first * cuts + (second + cuts - 1) / cuts * cuts) * heads);
+  }
+};
+DiffBwdGrid diff_bwd_grid(const sva_diff_args& a, int rows, int streamed, int ctas_per_sm);
 DiffBwdPlan diff_bwd_plan(int B, int N, int H, int d, sva_dtype_t dt);
 DiffBwdScratch diff_bwd_scratch(const sva_diff_args& a, void* scratch);
 cudaError_t diff_bwd(const sva_diff_args& a, const sva_diff_grads& g, int* status, void* scratch,

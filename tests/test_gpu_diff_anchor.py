@@ -128,6 +128,7 @@ SHAPES = [
     (2, 2, 700, 2), (1, 4, 5000, 3), (1, 3, 33, 1), (3, 1, 4095, 1),  # a handful, cut over clusters
     (1, 64, 64, 1), (1, 128, 128, 2), (1, 65, 129, 3), (2, 127, 63, 2), (1, 256, 192, 1),
     (2, 257, 1000, 1), (3, 333, 333, 2), (1, 5, 4097, 2),
+    (1, 3000, 70, 2), (2, 100, 9000, 1), (1, 2000, 2000, 1),  # few tiles, their streams cut over clusters
 ]
 
 
@@ -172,6 +173,17 @@ def test_padded_batch_of_a_few_queries(dtype, d, N, lens):
         t["k"][b, max(n, 0):] = float("nan")
         t["v"][b, max(n, 0):] = float("inf")
     compare(x, t, 2, dtype, lens=lens)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[6000, 0, 700], [5999, 65, 3000]])
+def test_padded_batch_of_cut_streams(dtype, lens):
+    x = make(3, 40, 6000, 1, 128, dtype, 16)
+    t = dev(x, dtype)
+    for b, n in enumerate(lens):
+        t["k"][b, n:] = float("nan")
+        t["v"][b, n:] = float("inf")
+    compare(x, t, 1, dtype, lens=lens)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
