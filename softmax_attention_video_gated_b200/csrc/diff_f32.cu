@@ -186,6 +186,16 @@ constexpr size_t fwd_smem() {
   return static_cast<size_t>(2 * FR + 4 * diff_f32_keys(D)) * (D + 4) * sizeof(float);
 }
 
+// The join of key parts as a call, for heads of 128: inlined, its registers make the key
+// loop spill 76 bytes (2 x 777 tokens, 4 heads: 136 us inlined, 132 as a call; 4,096 tokens,
+// where nothing joins: 1,204 and 1,196). Heads of 64 inline it: 55 us so, 57 as a call
+// (1,024 tokens, 4 heads).
+template <int D, int L>
+__device__ __noinline__ void cluster_join(const sva_diff_args& a, const DiffUnit& u, int split,
+                                          const float* os, const float* mls, float* w) {
+  cluster_finish<float, FR, D, L>(a, u, split, os, mls, w);
+}
+
 template <int D>
 __global__ void __launch_bounds__(128, 2)
     diff_fwd_kernel(const __grid_constant__ sva_diff_args a, float scale_log2, DiffWork wk) {
@@ -312,7 +322,10 @@ __global__ void __launch_bounds__(128, 2)
         *reinterpret_cast<float2*>(mls + 2 * (mp * FR + r + ln.g + 8 * i)) =
             make_float2(m[mp][i], l[mp][i]);
   if (wk.cluster) {
-    cluster_finish<float, FR, D, L>(a, u, wk.split, os, mls, mls + 4 * FR);
+    if constexpr (D == 128)
+      cluster_join<D, L>(a, u, wk.split, os, mls, mls + 4 * FR);
+    else
+      cluster_finish<float, FR, D, L>(a, u, wk.split, os, mls, mls + 4 * FR);
     return;
   }
   __syncwarp();  // a warp's rows are its own
