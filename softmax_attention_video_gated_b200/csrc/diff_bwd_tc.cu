@@ -20,8 +20,9 @@
 //     warp 1, round i:  S_i, dP_{i-1} in registers  ->  dP_i, S_{i+1}
 //     warp 3, round i:  dS_{i-1}, W_i stored        ->  dX += dS_{i-1} X', dV += W_i Y'
 // What one warp's MMAs need of the other's goes through the weights' barriers. dS goes
-// to TMEM and W to shared memory, in bf16, as A operands (a weight is off by 2^-9 of
-// itself at most, at random, as P is in the forward pass).
+// to TMEM and W to shared memory, in bf16, as A operands (a weight is off by 2^-8 of
+// itself at most, at random, as P is in the forward pass: 0.0029 of a gradient, relative
+// L2, where its own rounding alone is 0.0017).
 //
 // 8,190 tokens of 16 heads: 2.2 to 2.4 ms for both sides, 570 to 620 TFLOP/s of
 // the 10 d operations a pair that the gradients need; the steps there: MMAs behind elect.sync in uniform code
@@ -33,6 +34,8 @@
 // each thread reads by column stand in line behind them: without those reads the pass
 // would take 0.35 ms less, without the exponentials as much less. Queries standing: the
 // weights' instructions (0.93 ms of it). Sending exponentials to the FMA pipe costs here.
+// Few long tiles are cut along their stream over the CTAs of a cluster, which add up in
+// the order of the cuts: 64 queries against 4,000 keys, 8 heads, 89 -> 60 us.
 #include <algorithm>
 
 #include "diff_common.cuh"

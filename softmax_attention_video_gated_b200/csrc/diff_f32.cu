@@ -19,9 +19,13 @@
 // Scores leave the MMA in the layout that the next one takes as its left operand,
 // up to an exchange of the summed index that the right operand follows: P, W and
 // dS stay in registers.
-// 777 tokens, two batches, 4 heads of 128: forward 117 us and 21 for the merge of its
-// five parts, backward 272 us, 35 TFLOP/s in fp32; the tensor pipe is busy 41 to 43% of
-// the time, behind the operands' splitting and two warps a scheduler.
+// 777 tokens, two batches, 4 heads of 128: forward 115 us and 22 for the merge of its
+// five parts, backward 276 us, 35 TFLOP/s in fp32; the tensor pipe is busy 39 to 42% of
+// the time, behind the operands' splitting and two warps a scheduler. Parts that fit the
+// machine at once join in a cluster instead: 1,024 tokens, 4 heads of 64, 51 us in all
+// (2 us more with a merge; past one resident wave the clusters' waits made it slower).
+// Few long tiles of the backward pass are cut along their stream over a cluster: 64
+// queries against 4,000 keys, 8 heads of 128, 435 -> 198 us.
 #include <algorithm>
 
 #include "diff_common.cuh"

@@ -14,8 +14,9 @@
 // The MMA thread works on one map while the other's softmax runs. Running maximum
 // in the log2 domain, moved only when it grows by more than 8 (p <= 2^8
 // otherwise); l sums the unrounded p in fp32. Rounding p to bf16 for the product
-// is off by 2^-9 relative at most per weight, at random, so below the rounding of
-// the bf16 result.
+// is off by half a step, 2^-8 of the weight, at most and at random: the result is off by
+// 0.0026 (relative L2) where its own rounding alone is 0.0017. P in more bits would double
+// its product.
 // What bounds it: the exponentials, two per pair of a query and a key and product with
 // V. 8,190 tokens of 16 heads (1,024 CTAs) take 770 us, 1,070 TFLOP/s, 0.65 of the
 // measured bf16 peak; without exponentials it would take 595 us, with half of them 651.
