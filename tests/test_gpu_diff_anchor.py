@@ -390,6 +390,83 @@ def test_other_stream_graph_capture_and_two_calls_at_once(dtype):
     assert sva.sva_check_device_status(ws) == sva.SVA_OK
 
 
+# one query, a handful, a tile of queries against many keys, keys against many queries: each has
+# its kernel or its cuts
+CUT = [(2, 1, 3000, 2), (1, 4, 5000, 1), (2, 40, 6000, 1), (1, 3000, 70, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("flags", [0, sva.SVA_FLAG_LAMBDA_VALUE])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("B,N,keys,H", CUT)
+def test_lambda_forms_of_cut_work(dtype, flags, shared, B, N, keys, H):
+    x = make(B, N, keys, H, 128, dtype, 61, shared=shared)
+    x["lam"].ravel()[:2] = (-1.5, 0.0)[:x["lam"].size]
+    compare(x, dev(x, dtype), H, dtype, flags=flags)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,keys,H", CUT)
+def test_slices_of_cut_work(dtype, B, N, keys, H):
+    # keys and values, and their gradients, as column slices of one buffer: the same bits as from
+    # buffers of their own, and what lies between and behind is left as it was
+    x = make(B, N, keys, H, 128, dtype, 62)
+    t = dev(x, dtype)
+    D = H * 128
+    saved = new_saved(t, H)
+    out, _ = forward(t, H, saved)
+    g, _ = backward(t, H, saved)
+    kv = torch.full((B, keys, 2 * D + 32), float("nan"), device="cuda", dtype=TDT[dtype])
+    kv[..., :D], kv[..., D + 16:2 * D + 16] = t["k"], t["v"]
+    s = {**t, "k": kv[..., :D], "v": kv[..., D + 16:2 * D + 16]}
+    saved2 = new_saved(s, H)
+    out2, _ = forward(s, H, saved2)
+    assert torch.equal(out, out2) and all(torch.equal(a, b) for a, b in zip(saved, saved2))
+    dkv = torch.full((B, keys, 2 * D + 32), 7.0, device="cuda", dtype=TDT[dtype])
+    dq = torch.full((B, N, D + 16), 7.0, device="cuda", dtype=TDT[dtype])
+    dk, dv = dkv[..., :D], dkv[..., D + 16:2 * D + 16]
+    sva.sva_diff_anchor_bwd(s["q"], s["k"], s["v"], s["g"], s["lam"], s["dout"], saved2, dq[..., :D],
+                            dk, dv, torch.empty_like(s["g"]), torch.empty_like(s["lam"]), H)
+    for got, n in ((dq[..., :D], "dq"), (dk, "dk"), (dv, "dv")):
+        assert torch.equal(got, g[n]), n
+    assert torch.all(dkv[..., D:D + 16] == 7) and torch.all(dkv[..., 2 * D + 16:] == 7)
+    assert torch.all(dq[..., D:] == 7)
+
+
+@pytest.mark.parametrize("dtype, d", [("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("B,N,keys,H", CUT + [(1, 1024, 1024, 4)])
+def test_capture_of_cut_work(dtype, d, B, N, keys, H):
+    ts = [dev(make(B, N, keys, H, d, dtype, 63 + i), dtype) for i in range(2)]
+    t = {n: v.clone() for n, v in ts[0].items()}
+    saved = new_saved(t, H)
+    out = torch.empty_like(t["q"])
+    g = {n: torch.empty_like(t[s]) for n, s in zip(GRADS, ("q", "k", "v", "g", "lam"))}
+    dt = sva._dtype_code(t["q"])
+    ws = sva.workspace(sva.sva_diff_anchor_workspace_bytes(B, N, H, d, keys, dt))
+    wb = sva.workspace(sva.sva_diff_anchor_bwd_workspace_bytes(B, N, H, d, keys, dt))
+
+    def step():
+        sva.sva_diff_anchor_fwd(t["q"], t["k"], t["v"], t["g"], t["lam"], out, H, saved=saved, ws=ws)
+        sva.sva_diff_anchor_bwd(t["q"], t["k"], t["v"], t["g"], t["lam"], t["dout"], saved,
+                                g["dq"], g["dk"], g["dv"], g["dgate"], g["dlam"], H, ws=wb)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new in (ts[1], ts[0]):
+        for n in t:
+            t[n].copy_(new[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        own = new_saved(new, H)
+        eo, _ = forward(new, H, own)
+        eg, _ = backward(new, H, own)
+        assert torch.equal(out, eo) and all(torch.equal(a, b) for a, b in zip(saved, own))
+        assert all(torch.equal(g[n], eg[n]) for n in GRADS)
+
+
 def test_python_refusals():
     t = dev(make(1, 8, 8, 1, 128, "bf16", 1), "bf16")
     out = torch.empty_like(t["q"])
