@@ -72,7 +72,9 @@ __device__ __forceinline__ float half_sum(float v) {
 // heads of 128, bf16 (270 MB): 50 us; a warp a token 83 us, bound by its instructions.
 // delta_m is made
 // of the rounded dA, as dP is, so that dP - delta_m cancels where a map sits on one
-// key; dlambda is a result of its own and is made of the unrounded one.
+// key; dlambda is a result of its own and is made of the unrounded one (for the bf16 tiles
+// it goes to scratch, where the gradients' kernel adds what the forward pass's bf16 weights
+// left out of O_2).
 template <typename T, int Q>
 __global__ void __launch_bounds__(256)
     diff_prep_kernel(const __grid_constant__ sva_diff_args a, const __grid_constant__ sva_diff_grads g,
@@ -134,12 +136,11 @@ __global__ void __launch_bounds__(256)
     ws.stats[stat_at(bh, (a.N + 63) / 64, t) + l16 * 64] = v;
   }
   if (l16 == 0 && in) {
-    if (a.ldl != 0) {
-      const float f = (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : lam * (1.f - lam);
-      from_f32(static_cast<T*>(g.dlam) + row * g.lddl + h, dl * f);
-    } else {
+    if ((a.flags & SVA_FLAG_LAMBDA_VALUE) == 0) dl *= lam;
+    if (a.ldl != 0 && !diff_dlam_later(a))
+      from_f32(static_cast<T*>(g.dlam) + row * g.lddl + h, dl * dlambda_factor<T>(a, b, t, h));
+    else
       ws.dlam[static_cast<int64_t>(bh) * a.N + t] = dl;
-    }
   }
 }
 
@@ -162,9 +163,7 @@ __global__ void __launch_bounds__(1024) diff_dlam_kernel(const __grid_constant__
   if (threadIdx.x >= 32) return;
   s = warp_sum(part[threadIdx.x]);
   if (threadIdx.x != 0) return;
-  const float lam = lambda_of<T>(a, 0, 0, h);
-  const float f = (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : lam * (1.f - lam);
-  from_f32(static_cast<T*>(g.dlam) + h, s * f);
+  from_f32(static_cast<T*>(g.dlam) + h, s * dlambda_factor<T>(a, 0, 0, h));
 }
 
 template <typename T>
@@ -177,9 +176,6 @@ cudaError_t prepare(const sva_diff_args& a, const sva_diff_grads& g, const DiffB
     diff_prep_kernel<T, kHalf ? 1 : 2><<<grid, 256, 0, s>>>(a, g, ws, status);
   else
     diff_prep_kernel<T, 2><<<grid, 256, 0, s>>>(a, g, ws, status);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.ldl != 0) return e;
-  diff_dlam_kernel<T><<<static_cast<unsigned>(a.H), 1024, 0, s>>>(a, g, ws);
   return cudaGetLastError();
 }
 
@@ -285,10 +281,17 @@ cudaError_t diff_bwd(const sva_diff_args& a, const sva_diff_grads& g, int* statu
                      cudaStream_t s) {
   const bool tc = a.dtype == SVA_BF16;
   const DiffBwdScratch ws = diff_bwd_scratch(a, scratch);
-  const cudaError_t e = tc ? prepare<__nv_bfloat16>(a, g, ws, status, s) : prepare<float>(a, g, ws, status, s);
+  cudaError_t e = tc ? prepare<__nv_bfloat16>(a, g, ws, status, s) : prepare<float>(a, g, ws, status, s);
   if (e != cudaSuccess) return e;
-  if (a.N <= kDiffFewRows) return diff_bwd_few(a, g, scratch, s);
-  return tc ? diff_bwd_bf16(a, g, status, scratch, s) : diff_bwd_f32(a, g, scratch, s);
+  e = a.N <= kDiffFewRows ? diff_bwd_few(a, g, scratch, s)
+      : tc                ? diff_bwd_bf16(a, g, status, scratch, s)
+                          : diff_bwd_f32(a, g, scratch, s);
+  if (e != cudaSuccess || a.ldl != 0) return e;
+  if (tc)
+    diff_dlam_kernel<__nv_bfloat16><<<static_cast<unsigned>(a.H), 1024, 0, s>>>(a, g, ws);
+  else
+    diff_dlam_kernel<float><<<static_cast<unsigned>(a.H), 1024, 0, s>>>(a, g, ws);
+  return cudaGetLastError();
 }
 
 }  // namespace sva

@@ -24,6 +24,17 @@
 // itself at most, at random, as P is in the forward pass: 0.0029 of a gradient, relative
 // L2, where its own rounding alone is 0.0017).
 //
+// dlambda_t = -dA_t . O_2[t] = -sum_s P_2 dP is a sum whose terms cancel, and a lambda shared
+// by all tokens adds up tokens that cancel again, while the errors that O_2 brings from the
+// forward pass's bf16 weights (0.0015 of a token's terms, at random) do not: of 302 training
+// steps with any number of heads seven were off by more than 0.005, one by 0.024. The
+// queries' side has P_2 and dP in fp32, so it adds what O_2 missed: with delta_2 = r . O_2,
+// r the rounded dA,
+//     sum_s P_2 dP = delta_2 + sum_s P_2 (dP - delta_2)
+// where the last sum would be zero for an exact O_2, and an error of sum_s P_2 times it
+// cancels. It is one addition per pair and map 2, on dS_2 before its rounding, and takes 35
+// us of a training step of 8,190 tokens and 16 heads (3.40 -> 3.44 ms).
+//
 // 8,190 tokens of 16 heads: 2.2 to 2.4 ms for both sides, 570 to 620 TFLOP/s of
 // the 10 d operations a pair that the gradients need; the steps there: MMAs behind elect.sync in uniform code
 // 3.2 -> 2.8 ms, two warps of weights a scheduler -> four without a spilled register
@@ -108,7 +119,8 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
   const CUtensorMap &map_x2 = KV ? maps.q : maps.k, &map_y2 = KV ? maps.da : maps.v;
   using L = Layout<KV>;
   constexpr int NC = KV ? 2 * HD : HD;  // columns of the results
-  static_assert(BR * (NC + 4) * 4 <= L::TAIL - L::RING, "a share fits the ring's place");
+  constexpr int SUMS_AT = BR * (NC + 4);  // behind a share of the results: WGS sums a row
+  static_assert((SUMS_AT + (KV ? 0 : WGS * BR)) * 4 <= L::TAIL - L::RING, "a share fits the ring's place");
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   Tail* tl = reinterpret_cast<Tail*>(smem + L::TAIL);
@@ -326,6 +338,7 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
     const int n_rows = KV ? Nk : a.N;
     const uint64_t scale2 = f2pack(scale_log2, scale_log2);
     uint64_t nlse1 = 0, nlse2 = 0, nd1 = 0, nd2 = 0, nl = 0;  // queries stand: this row's
+    uint64_t off2 = 0;  // and its sum of P_2 (dP - delta_2), with lambda in P_2 or not, see below
     if (!KV && n > 0) {
       // the first two warpgroups bring Q, the others dA, half of the columns each
       const bool in = row < a.N;
@@ -355,7 +368,9 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
     const uint64_t minus_one = f2pack(-1.f, -1.f);
     const bool raw = (a.flags & SVA_FLAG_LAMBDA_VALUE) != 0;  // else the last statistic is -1
     bool ok = true;
-    uint64_t p1[COLS / 2], q2[COLS / 2];  // P_1 and -lambda P_2 of a block
+    // P_1 and, keys standing, -lambda P_2 of a block; queries standing the last factor comes
+    // later: P_2, with a sigmoid's lambda in its exponent
+    uint64_t p1[COLS / 2], q2[COLS / 2];
     const float* stat0 = reinterpret_cast<const float*>(smem + L::STAT) + COLS * part;
     const float* stat = stat0;  // block i's statistics; prev: block i - 1's
     const float* prev = stat0 + (STAGES - 1) * (STAT_BYTES / 4);
@@ -374,35 +389,44 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
         uint32_t dp[COLS];
         tmem_ld16(lane_base + TM_DP + COLS * part, dp);
         tmem_wait_ld();
-        ulonglong2 g1, g2;  // two pairs of queries' statistics at a time
+        // queries stand: keys of block i - 1 that count, of this warpgroup's
+        const int left = KV ? COLS : valid - (j0 + i - 1) * BS - COLS * part;
+        auto make_ds = [&](auto all) {
+          ulonglong2 g1, g2;  // two pairs of queries' statistics at a time
 #pragma unroll
-        for (int k = 0; k < COLS / 2; ++k) {
-          if (KV) {
-            if (k % 2 == 0) {
-              g1 = *reinterpret_cast<const ulonglong2*>(prev + 128 + 2 * k);
-              g2 = *reinterpret_cast<const ulonglong2*>(prev + 192 + 2 * k);
+          for (int k = 0; k < COLS / 2; ++k) {
+            if (KV) {
+              if (k % 2 == 0) {
+                g1 = *reinterpret_cast<const ulonglong2*>(prev + 128 + 2 * k);
+                g2 = *reinterpret_cast<const ulonglong2*>(prev + 192 + 2 * k);
+              }
+              nd1 = k % 2 == 0 ? g1.x : g1.y;
+              nd2 = k % 2 == 0 ? g2.x : g2.y;
             }
-            nd1 = k % 2 == 0 ? g1.x : g1.y;
-            nd2 = k % 2 == 0 ? g2.x : g2.y;
-          }
-          float x0, x1, y0, y1;
-          const uint64_t dpp = f2pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1]));
-          f2unpack(mul_f2(p1[k], add_f2(dpp, nd1)), x0, x1);
-          f2unpack(mul_f2(q2[k], add_f2(dpp, nd2)), y0, y1);
-          d1[k] = pack_bf16x2(x0, x1);
-          d2[k] = pack_bf16x2(y0, y1);
-        }
-        if (!KV) {  // keys of block i - 1 that count
-          const int left = valid - (j0 + i - 1) * BS - COLS * part;
-          if (left < COLS) {
-#pragma unroll
-            for (int k = 0; k < COLS / 2; ++k) {
-              const uint32_t keep = (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
-              d1[k] &= keep;
-              d2[k] &= keep;
+            float x0, x1, y0, y1;
+            const uint64_t dpp = f2pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1]));
+            const uint64_t ds1 = mul_f2(p1[k], add_f2(dpp, nd1));
+            uint64_t ds2 = mul_f2(q2[k], add_f2(dpp, nd2));
+            if (!decltype(all)::value) {
+              f2unpack(ds2, y0, y1);
+              ds2 = f2pack(2 * k < left ? y0 : 0.f, 2 * k + 1 < left ? y1 : 0.f);
             }
+            if (!KV) {
+              off2 = add_f2(off2, ds2);
+              ds2 = mul_f2(ds2, nl);
+            }
+            f2unpack(ds1, x0, x1);
+            f2unpack(ds2, y0, y1);
+            d1[k] = pack_bf16x2(x0, x1);
+            d2[k] = pack_bf16x2(y0, y1);
+            if (!decltype(all)::value)
+              d1[k] &= (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
           }
-        }
+        };
+        if (left < COLS)
+          make_ds(Int<0>());
+        else
+          make_ds(Int<1>());
       }
       if (i < n) {
         // the stage's statistics landed before the scores were made of its rows, but
@@ -439,8 +463,9 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
           f2unpack(fma_f2(f2pack(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])), scale2,
                           nlse2), y0, y1);
           p1[k] = f2pack(ex2_mufu(x0), ex2_mufu(x1));
-          q2[k] = mul_f2(f2pack(ex2_mufu(y0), ex2_mufu(y1)), nl);
+          q2[k] = f2pack(ex2_mufu(y0), ex2_mufu(y1));
           if (KV) {
+            q2[k] = mul_f2(q2[k], nl);
             f2unpack(add_f2(p1[k], q2[k]), x0, x1);
             wk[k] = pack_bf16x2(x0, x1);
           }
@@ -477,6 +502,11 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(&tl->acc_done, 0, abort_flag, status, WHERE_DIFF_BWD));
     tc_fence_after();
+    if (!KV) {  // off2 of this warpgroup's columns, behind the place of dQ's shares
+      float x0, x1;
+      f2unpack(off2, x0, x1);
+      reinterpret_cast<float*>(smem + L::RING)[SUMS_AT + part * BR + r] = x0 + x1;
+    }
     // keys stand: half of dK or dV a warpgroup; queries stand: a quarter of dQ
     const int64_t at = static_cast<int64_t>(b) * n_rows + row;
     __nv_bfloat16* dst;
@@ -528,6 +558,23 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
+  // queries stand: dlambda of row `row`, its sums added up in the order of cuts and warpgroups
+  auto finish_dlam = [&](const float* sums, int row) {
+    float off = 0.f;
+    for (int p = 0; p < u.cuts; ++p)
+      for (int w = 0; w < WGS; ++w)
+        off += u.cuts > 1 ? ld_cluster(sums + w * BR, static_cast<uint32_t>(p)) : sums[w * BR];
+    float* dl = ws.dlam + static_cast<int64_t>(bh) * a.N + row;
+    const float x = *dl - off;
+    if (a.ldl == 0)
+      *dl = x;
+    else
+      from_f32(static_cast<__nv_bfloat16*>(g.dlam) + (static_cast<int64_t>(b) * a.N + row) * g.lddl + h,
+               x * dlambda_factor<__nv_bfloat16>(a, b, row, h));
+  };
+  const float* sums = reinterpret_cast<const float*>(smem + L::RING) + SUMS_AT + threadIdx.x;
+  const bool sums_row = !KV && threadIdx.x < BR && r0 + static_cast<int>(threadIdx.x) < a.N;
+  if (u.cuts == 1 && sums_row) finish_dlam(sums, r0 + static_cast<int>(threadIdx.x));
   if (u.cuts > 1) {
     // the cuts of a tile are a cluster; the first adds up the shares, in their order
     cluster_sync();
@@ -548,6 +595,7 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
                                       : static_cast<__nv_bfloat16*>(g.dv) + at * g.lddv;
         store4(dst + h * HD + c % HD, x);
       }
+      if (sums_row) finish_dlam(sums, r0 + static_cast<int>(threadIdx.x));
     }
     cluster_sync();  // nobody leaves while its shared memory is read
   }

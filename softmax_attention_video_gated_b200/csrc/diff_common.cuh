@@ -71,6 +71,13 @@ __device__ __forceinline__ float lambda_of(const sva_diff_args& a, int b, int64_
   return (a.flags & SVA_FLAG_LAMBDA_VALUE) ? x : sigmoid_f(x);
 }
 
+// What dlambda's sum is multiplied by in the end, 1 for lambda as a value: the sum for a
+// sigmoid's lambda carries the factor lambda already (dsigma = lambda (1 - lambda)).
+template <typename T>
+__device__ __forceinline__ float dlambda_factor(const sva_diff_args& a, int b, int64_t t, int h) {
+  return (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : 1.f - lambda_of<T>(a, b, t, h);
+}
+
 // One query row's end: both maps normalised, lambda, gate, stores, saved tensors.
 // o1, o2: this thread's four columns [c, c + 4) of the head (unnormalised).
 template <typename T>

@@ -180,8 +180,14 @@ struct DiffBwdScratch {
   // [B*H][tiles of 64 queries][5][64]: -lse_1 log2 e, -lse_2 log2 e + log2 lambda,
   // -delta_m, -1; with lambda given as a value the second without it, the last -lambda
   float* stats;
-  float* dlam;   // [B*H][N]: dlambda per token, where one lambda is shared by all
+  // [B*H][N]: -dA . O_2 per token (times a sigmoid's lambda), where one lambda is shared by
+  // all or the gradients' kernel corrects it
+  float* dlam;
 };
+// bf16 tiles: O_2 was made of bf16 weights
+__host__ __device__ inline bool diff_dlam_later(const sva_diff_args& a) {
+  return a.dtype == SVA_BF16 && a.N > kDiffFewRows;
+}
 // One launch of the backward tiles: `first` tiles a (batch, head) of the side whose
 // tiles take longer (their streamed side is the longer one), each cut `cuts` ways along
 // that stream where there are too few of them, the cuts being a cluster; then the
