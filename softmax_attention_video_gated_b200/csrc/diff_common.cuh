@@ -19,7 +19,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 16 a cycle and SM, and two maps take twice the exponentials of one per product with
 // V: a kernel that is bound by them gives a share to this form.
 __device__ __forceinline__ void ex2_poly2(float x0, float x1, float& p0, float& p1) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-126.f));  // a NaN stays one, and ends non-finite
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-126.f));  // a NaN ends as the largest number
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-126.f));
   const uint64_t x = f2pack(x0, x1);
   const uint64_t t = add_f2(x, f2pack(12582912.f, 12582912.f));
@@ -78,12 +78,16 @@ __device__ __forceinline__ float dlambda_factor(const sva_diff_args& a, int b, i
   return (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : 1.f - lambda_of<T>(a, b, t, h);
 }
 
+// 1 / l of a row's sum. Without a key l is zero, and so is the row; with keys it is 2^-8 at
+// least (the running maximum's threshold), or not a number where a score was none.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
+
 // One query row's end: both maps normalised, lambda, gate, stores, saved tensors.
 // o1, o2: this thread's four columns [c, c + 4) of the head (unnormalised).
 template <typename T>
 __device__ __forceinline__ void finish4(const sva_diff_args& a, int b, int h, int64_t t, int c,
                                         float4 o1, float4 o2, float l1, float l2, float lam) {
-  const float i1 = l1 > 0.f ? 1.0f / l1 : 0.f, i2 = l2 > 0.f ? 1.0f / l2 : 0.f;
+  const float i1 = inverse_sum(l1), i2 = inverse_sum(l2);
   o1 = make_float4(o1.x * i1, o1.y * i1, o1.z * i1, o1.w * i1);
   o2 = make_float4(o2.x * i2, o2.y * i2, o2.z * i2, o2.w * i2);
   const int64_t row = static_cast<int64_t>(b) * a.N + t;
@@ -107,7 +111,7 @@ __device__ __forceinline__ void finish_lse(const sva_diff_args& a, int m, int b,
                                            float mx, float l) {
   if (a.lse != nullptr)
     a.lse[((static_cast<int64_t>(m) * a.B + b) * a.H + h) * a.N + t] =
-        l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
 }
 
 constexpr int kStats = 5;
@@ -224,7 +228,8 @@ __device__ __forceinline__ void cluster_finish(const sva_diff_args& a, const Dif
     float l = 0.f;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      // a part without keys has a weight of zero, and its outputs are zero
+      // a part without keys has a weight of zero, and its outputs are zero; one whose scores
+      // are not numbers has no maximum either, but its sum and outputs are none, and stay so
       const float wp = ml[p].x == -INFINITY ? 0.f : exp2f(ml[p].x - mx);
       l = fmaf(wp, ml[p].y, l);
       w[(mp * ROWS + r) * 9 + p] = wp;
