@@ -30,10 +30,9 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const sva_diff_args a, 
       ml = *reinterpret_cast<const float2*>(diff_part(wk, a.d, su, lane, mm) + wk.rows * a.d + 2 * r);
     mx[mm] = warp_max(ml.x);
     // a part has no keys where its sum is zero; one whose scores are not numbers has a maximum
-    // of -infinity too, and must not be lost
-    const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - mx[mm]);
+    // of -infinity too, and must not be lost: a part with keys has a weight above zero
+    const float w = ml.y == 0.f ? 0.f : fmaxf(exp2f(ml.x - mx[mm]), 0x1p-126f);
     l[mm] = warp_sum(w * ml.y);
-    const uint32_t live = __ballot_sync(0xffffffffu, ml.y != 0.f);
     o[mm] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int p = 0; p < wk.split; ++p) {
@@ -42,11 +41,10 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const sva_diff_args a, 
         x = *reinterpret_cast<const float4*>(diff_part(wk, a.d, su, p, mm) + r * a.d + 4 * lane);
       // a part without keys has not written its O: whatever is there does not count
       const float wp = __shfl_sync(0xffffffffu, w, p);
-      const bool on = (live >> p) & 1;
-      o[mm].x = fmaf(wp, on ? x.x : 0.f, o[mm].x);
-      o[mm].y = fmaf(wp, on ? x.y : 0.f, o[mm].y);
-      o[mm].z = fmaf(wp, on ? x.z : 0.f, o[mm].z);
-      o[mm].w = fmaf(wp, on ? x.w : 0.f, o[mm].w);
+      o[mm].x = fmaf(wp, wp != 0.f ? x.x : 0.f, o[mm].x);
+      o[mm].y = fmaf(wp, wp != 0.f ? x.y : 0.f, o[mm].y);
+      o[mm].z = fmaf(wp, wp != 0.f ? x.z : 0.f, o[mm].z);
+      o[mm].w = fmaf(wp, wp != 0.f ? x.w : 0.f, o[mm].w);
     }
   }
   if (4 * lane < a.d)
