@@ -573,12 +573,13 @@ __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_
       if (rr >= n_rows) continue;
       const int64_t row = static_cast<int64_t>(b) * n_rows + rr;
       const int col = h * D + 8 * n + 2 * ln.t;
-      if (KV) {
+      if constexpr (KV) {
+        // rows behind the last key are zero, also where a query's values are no numbers
+        const bool in = rr < valid;
         *reinterpret_cast<float2*>(static_cast<float*>(g.dk) + row * g.lddk + col) =
-            make_float2(scale * acc[n][2 * i], scale * acc[n][2 * i + 1]);
-        if constexpr (KV)
-          *reinterpret_cast<float2*>(static_cast<float*>(g.dv) + row * g.lddv + col) =
-              make_float2(accv[n][2 * i], accv[n][2 * i + 1]);
+            make_float2(in ? scale * acc[n][2 * i] : 0.f, in ? scale * acc[n][2 * i + 1] : 0.f);
+        *reinterpret_cast<float2*>(static_cast<float*>(g.dv) + row * g.lddv + col) =
+            make_float2(in ? accv[n][2 * i] : 0.f, in ? accv[n][2 * i + 1] : 0.f);
       } else {
         *reinterpret_cast<float2*>(static_cast<float*>(g.dq) + row * g.lddq + col) =
             make_float2(scale * acc[n][2 * i], scale * acc[n][2 * i + 1]);

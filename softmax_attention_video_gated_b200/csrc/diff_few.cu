@@ -221,12 +221,17 @@ __global__ void __launch_bounds__(32 * WARPS)
   }
 }
 
-__device__ __forceinline__ void narrow16(float* p, const float (&f)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+template <typename T>
+__device__ __forceinline__ uint4 narrow16(const float (&f)[16 / sizeof(T)]);
+template <>
+__device__ __forceinline__ uint4 narrow16<float>(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
 }
-__device__ __forceinline__ void narrow16(__nv_bfloat16* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+template <>
+__device__ __forceinline__ uint4 narrow16<__nv_bfloat16>(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
 }
 
 template <typename T, int D, int R>
@@ -317,7 +322,8 @@ __global__ void __launch_bounds__(32 * WARPS)
         // this map's weight: P_1, or -lambda P_2
         const float p = key < valid ? nl[r] * exp2f(s[r] + nlse[r]) : 0.f;
         const float w = p + __shfl_xor_sync(0xffffffffu, p, LPK / 2);
-        const float ds = p * (dp[r] + nd[r]), dsq = ds * 0.6931471805599453f;  // q is in log2 units
+        // q is in log2 units
+        const float ds = key < valid ? p * (dp[r] + nd[r]) : 0.f, dsq = ds * 0.6931471805599453f;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           dk[e] = fmaf(dsq, q[r][e], dk[e]);
@@ -326,8 +332,12 @@ __global__ void __launch_bounds__(32 * WARPS)
         }
       }
       if (key < k1) {
-        narrow16(dkp + key * g.lddk, dk);
-        narrow16(dvp + key * g.lddv, dv);
+        // zeros behind the last key, also where q or dA is not a number
+        uint4* dko = reinterpret_cast<uint4*>(dkp + key * g.lddk);
+        uint4* dvo = reinterpret_cast<uint4*>(dvp + key * g.lddv);
+        const bool in = key < valid;
+        *dko = in ? narrow16<T>(dk) : make_uint4(0, 0, 0, 0);
+        *dvo = in ? narrow16<T>(dv) : make_uint4(0, 0, 0, 0);
       }
     }
   }

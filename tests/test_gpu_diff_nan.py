@@ -105,3 +105,17 @@ def test_no_keys_are_not_a_nan(dtype, d, B, N, keys, H):
     r = step(t, H)
     assert all(float(r[n][0].abs().max()) == 0 for n in ("out", "o1", "o2", "dq", "dk", "dv", "dgate", "dlam"))
     assert torch.all(r["lse"][:, 0] == -math.inf) and torch.isfinite(r["lse"][:, 1]).all()
+
+
+@pytest.mark.parametrize("what", ["q", "dout"])
+@pytest.mark.parametrize("dtype,d,B,N,keys,H", PLANS)
+def test_rows_behind_the_last_key_are_zero_whatever_the_queries_hold(dtype, d, B, N, keys, H, what):
+    t = make(dtype, d, max(B, 2), N, keys, H)
+    x = t[what].clone()
+    x[:, N // 2] = math.nan
+    for lens in ([keys, 0], [keys - 3, keys]):
+        t["lens"][:2] = torch.tensor(lens)
+        r = step({**t, what: x}, H)
+        for b in range(2):
+            for n in ("dk", "dv"):
+                assert torch.all(r[n][b, lens[b]:] == 0), (n, b)
