@@ -268,8 +268,14 @@ def _rows(t, B: int, N: int):
     return t.stride(1)
 
 
-def workspace(nbytes: int, device=None):
+def workspace(nbytes: int, device=None, stream=None):
+    """A workspace of `nbytes` for calls on `stream` (default: the current one). It belongs to that
+    stream: its memory is not in use by other work when the call begins, nor given to other work
+    before the call ends, whenever the caller lets go of it."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return workspace(nbytes, device)
     return torch.empty(max(int(nbytes), SVA_STATUS_BYTES), dtype=torch.uint8,
                        device=device if device is not None else "cuda")
 
@@ -328,7 +334,7 @@ def sva_linear_attn_fwd(q, k, v, gate, out, H: int, residual=None, eps: float = 
     are scaled by sigmoid(wgate[b, t, h])."""
     a = _attn_args(q, k, v, gate, out, H, residual, eps, 0.0, flags, wgate)
     need = sva_linear_attn_workspace_bytes(a.B, a.N, a.H, a.d, a.dtype)
-    ws = workspace(need, q.device) if ws is None else ws
+    ws = workspace(need, q.device, stream) if ws is None else ws
     _check(_lib().sva_linear_attn_fwd(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)),
            "sva_linear_attn_fwd")
     return ws
@@ -344,7 +350,7 @@ def sva_linear_attn_state_fwd(k, v, state, H: int, flags: int = 0, wgate=None, w
     a = _attn_args(None, k, v, None, None, H, None, 0.0, 0.0, flags, wgate)
     _check_state(state, a)
     need = sva_linear_attn_workspace_bytes(a.B, a.N, a.H, a.d, a.dtype)
-    ws = workspace(need, k.device) if ws is None else ws
+    ws = workspace(need, k.device, stream) if ws is None else ws
     _check(_lib().sva_linear_attn_state_fwd(ctypes.byref(a), _ptr(state), _ptr(ws), ws.numel(),
                                             _stream(stream)), "sva_linear_attn_state_fwd")
     return ws
@@ -356,7 +362,7 @@ def sva_linear_attn_readout_fwd(q, gate, out, state, H: int, residual=None, eps:
     a = _attn_args(q, None, None, gate, out, H, residual, eps, 0.0, flags)
     _check_state(state, a)
     need = sva_linear_attn_workspace_bytes(a.B, a.N, a.H, a.d, a.dtype)
-    ws = workspace(need, q.device) if ws is None else ws
+    ws = workspace(need, q.device, stream) if ws is None else ws
     _check(_lib().sva_linear_attn_readout_fwd(ctypes.byref(a), _ptr(state), _ptr(ws), ws.numel(),
                                               _stream(stream)), "sva_linear_attn_readout_fwd")
     return ws
@@ -384,7 +390,7 @@ def sva_softmax_anchor_fwd(q, k, v, gate, out, H: int, residual=None, scale: flo
     """Gated softmax anchor: out = softmax(scale Q K^T) V * sigmoid(G) (+ residual)."""
     a = _attn_args(q, k, v, gate, out, H, residual, 0.0, scale, 0)
     need = int(_lib().sva_softmax_anchor_workspace_bytes(a.B, a.N, a.H, a.d, a.dtype))
-    ws = workspace(need, q.device) if ws is None else ws
+    ws = workspace(need, q.device, stream) if ws is None else ws
     _check(_lib().sva_softmax_anchor_fwd(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)),
            "sva_softmax_anchor_fwd")
     return ws
@@ -471,10 +477,10 @@ def _lam(lam, B: int, N: int, H: int, dt, dev: int, name: str):
     return _act(lam, B, N, H, dt, dev, name)
 
 
-def _space(ws, need, dev: int):
+def _space(ws, need, dev: int, stream):
     """The call's workspace, made to measure where none is given."""
     if ws is None:
-        return workspace(need(), f"cuda:{dev}")
+        return workspace(need(), f"cuda:{dev}", stream)
     if ws.get_device() != dev:
         raise ValueError(f"ws must be on cuda:{dev}")
     return ws
@@ -513,7 +519,8 @@ def sva_diff_anchor_fwd(q, k, v, gate, lam, out, H: int, key_lens=None, scale: f
     [B, N, >=H] or [H] (lambda itself with SVA_FLAG_LAMBDA_VALUE). key_lens [B] int32: keys
     of each batch. saved (o1, o2, lse): written for sva_diff_anchor_bwd."""
     a, dev = _diff_args(q, k, v, gate, lam, out, H, key_lens, scale, flags, saved)
-    ws = _space(ws, lambda: sva_diff_anchor_workspace_bytes(a.B, a.N, a.H, a.d, a.n_keys, a.dtype), dev)
+    ws = _space(ws, lambda: sva_diff_anchor_workspace_bytes(a.B, a.N, a.H, a.d, a.n_keys, a.dtype), dev,
+                stream)
     _check(_lib().sva_diff_anchor_fwd(ctypes.byref(a), ws.data_ptr(), ws.numel(), _here(stream, dev)),
            "sva_diff_anchor_fwd")
     return ws
@@ -536,7 +543,8 @@ def sva_diff_anchor_bwd(q, k, v, gate, lam, dout, saved, dq, dk, dv, dgate, dlam
     g = DiffGrads(*_act(dout, B, N, D, dt, dev, "dout"), *_act(dq, B, N, D, dt, dev, "dq"),
                   *_act(dk, B, Nk, D, dt, dev, "dk"), *_act(dv, B, Nk, D, dt, dev, "dv"),
                   *_act(dgate, B, N, D, dt, dev, "dgate"), *_lam(dlam, B, N, H, dt, dev, "dlam"))
-    ws = _space(ws, lambda: sva_diff_anchor_bwd_workspace_bytes(B, N, H, a.d, a.n_keys, a.dtype), dev)
+    ws = _space(ws, lambda: sva_diff_anchor_bwd_workspace_bytes(B, N, H, a.d, a.n_keys, a.dtype), dev,
+                stream)
     _check(_lib().sva_diff_anchor_bwd(ctypes.byref(a), ctypes.byref(g), ws.data_ptr(), ws.numel(),
                                       _here(stream, dev)), "sva_diff_anchor_bwd")
     return ws
@@ -606,7 +614,7 @@ def sva_block_norm_bwd(h_out, stats, dh, dh_out=None, o=None, do=None, du=None, 
                        _flat(dw_post, (D,), f32, dev, "dw_post"), _flat(dgate, (B, D), f32, dev, "dgate"),
                        _flat(dw_pre, (D,), f32, dev, "dw_pre"), _flat(dscale, (B, D), f32, dev, "dscale"),
                        _flat(dshift, (B, D), f32, dev, "dshift"))
-    ws = _space(ws, lambda: sva_block_norm_bwd_workspace_bytes(B, N, D), dev)
+    ws = _space(ws, lambda: sva_block_norm_bwd_workspace_bytes(B, N, D), dev, stream)
     _check(_lib().sva_block_norm_bwd(ctypes.byref(a), ctypes.byref(g), ws.data_ptr(), ws.numel(),
                                      _here(stream, dev)), "sva_block_norm_bwd")
     return ws
@@ -618,7 +626,7 @@ def sva_projection_fwd(x, w, y, relu_cols: int = 0, ws=None, stream=None):
     Nout = w.shape[0]
     if w.shape[1] != K or not w.is_contiguous() or y.shape != (M, Nout):
         raise ValueError("shape mismatch")
-    ws = workspace(SVA_STATUS_BYTES, x.device) if ws is None else ws
+    ws = workspace(SVA_STATUS_BYTES, x.device, stream) if ws is None else ws
     _check(_lib().sva_projection_fwd(_ptr(x), x.stride(0), _ptr(w), M, Nout, K, _ptr(y),
                                      y.stride(0), relu_cols, _dtype_code(x), _ptr(ws), ws.numel(),
                                      _stream(stream)), "sva_projection_fwd")
@@ -629,7 +637,7 @@ def sva_projection_residual_fwd(x, w, h, h_copy=None, ws=None, stream=None):
     """h += x W^T (h fp32); h_copy = dtype(h) when given."""
     M, K = x.shape
     Nout = w.shape[0]
-    ws = workspace(SVA_STATUS_BYTES, x.device) if ws is None else ws
+    ws = workspace(SVA_STATUS_BYTES, x.device, stream) if ws is None else ws
     _check(_lib().sva_projection_residual_fwd(
         _ptr(x), x.stride(0), _ptr(w), M, Nout, K, _ptr(h), h.stride(0), _ptr(h_copy),
         h_copy.stride(0) if h_copy is not None else 0, _dtype_code(x), _ptr(ws), ws.numel(),
@@ -642,7 +650,7 @@ def sva_attnres_keys(s_b, w_r, k_b, ws=None, stream=None):
     rows, D = s_b.shape
     dt = _dtype_code(s_b)
     need = int(_lib().sva_attnres_keys_workspace_bytes(D, dt))
-    ws = workspace(need, s_b.device) if ws is None else ws
+    ws = workspace(need, s_b.device, stream) if ws is None else ws
     _check(_lib().sva_attnres_keys(_ptr(s_b), _ptr(w_r), _ptr(k_b), rows, D, dt, _ptr(ws),
                                    ws.numel(), _stream(stream)), "sva_attnres_keys")
     return ws
@@ -732,7 +740,7 @@ def sva_hybrid_stack_fwd(stack: Stack, x, y, ws=None, stream=None):
     """y = the hybrid stack applied to x ([B, N, D], contiguous, dtype of the weights)."""
     if not (x.is_contiguous() and y.is_contiguous()):
         raise ValueError("x and y must be contiguous [B, N, D]")
-    ws = workspace(stack.workspace_bytes(), x.device) if ws is None else ws
+    ws = workspace(stack.workspace_bytes(), x.device, stream) if ws is None else ws
     _check(_lib().sva_hybrid_stack_fwd(ctypes.byref(stack.desc), _ptr(x), _ptr(y), _ptr(ws),
                                        ws.numel(), _stream(stream)), "sva_hybrid_stack_fwd")
     return ws
@@ -754,9 +762,9 @@ def sva_hybrid_stack_fwd_host(stack: Stack, xs_host: Sequence, ys_host: Sequence
             raise ValueError("host batches must be contiguous CPU tensors")
     torch = _torch()
     dev = torch.device("cuda", torch.cuda.current_device())
-    ws = workspace(stack.workspace_bytes(), dev) if ws is None else ws
+    ws = workspace(stack.workspace_bytes(), dev, stream) if ws is None else ws
     if staging is None:
-        staging = workspace(sva_hybrid_stack_host_staging_bytes(stack), dev)
+        staging = workspace(sva_hybrid_stack_host_staging_bytes(stack), dev, stream)
     n = len(xs_host)
     xp = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in xs_host])
     yp = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in ys_host])
