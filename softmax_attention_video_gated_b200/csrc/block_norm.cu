@@ -181,10 +181,9 @@ struct Group {
       v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
     if (W == 1) return v;
-    if (lane_id() == 0) {
-      sums->part[slot][0][warp_in] = v.x;
-      sums->part[slot][1][warp_in] = v.y;
-    }
+    // all lanes hold the sum and write it: bar.sync wants the whole warp at once
+    sums->part[slot][0][warp_in] = v.x;
+    sums->part[slot][1][warp_in] = v.y;
     named_barrier_sync(bar, 32 * W);
     v = make_float2(joined(0), joined(1));
     slot ^= 1;
@@ -194,7 +193,7 @@ struct Group {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (W == 1) return v;
-    if (lane_id() == 0) sums->part[slot][0][warp_in] = v;
+    sums->part[slot][0][warp_in] = v;
     named_barrier_sync(bar, 32 * W);
     v = joined(0);
     slot ^= 1;
