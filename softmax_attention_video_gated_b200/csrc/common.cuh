@@ -518,7 +518,9 @@ __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
   return v;
 }
 
+// The .aligned forms want the whole warp at once, also behind loops that its lanes leave apart.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
 }

@@ -352,6 +352,7 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
         const uint4 w = in ? p[i] : make_uint4(0, 0, 0, 0);
         x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
       }
+      __syncwarp();  // rows behind the last query loaded nothing
       tmem_st32(lane_base + TM_X + 32 * part, x);
       tmem_wait_st();
       tc_fence_before();
@@ -535,20 +536,20 @@ __device__ __forceinline__ void bwd_tile(const Maps& maps, const sva_diff_args& 
               zero ? make_float4(0.f, 0.f, 0.f, 0.f)
                    : make_float4(f * __uint_as_float(o[4 * k]), f * __uint_as_float(o[4 * k + 1]),
                                  f * __uint_as_float(o[4 * k + 2]), f * __uint_as_float(o[4 * k + 3]));
-        continue;
-      }
-      if (row >= n_rows) continue;
+      } else if (row < n_rows) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (!zero) {
-          v.x = pack_bf16x2(f * __uint_as_float(o[8 * k]), f * __uint_as_float(o[8 * k + 1]));
-          v.y = pack_bf16x2(f * __uint_as_float(o[8 * k + 2]), f * __uint_as_float(o[8 * k + 3]));
-          v.z = pack_bf16x2(f * __uint_as_float(o[8 * k + 4]), f * __uint_as_float(o[8 * k + 5]));
-          v.w = pack_bf16x2(f * __uint_as_float(o[8 * k + 6]), f * __uint_as_float(o[8 * k + 7]));
+        for (int k = 0; k < 4; ++k) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (!zero) {
+            v.x = pack_bf16x2(f * __uint_as_float(o[8 * k]), f * __uint_as_float(o[8 * k + 1]));
+            v.y = pack_bf16x2(f * __uint_as_float(o[8 * k + 2]), f * __uint_as_float(o[8 * k + 3]));
+            v.z = pack_bf16x2(f * __uint_as_float(o[8 * k + 4]), f * __uint_as_float(o[8 * k + 5]));
+            v.w = pack_bf16x2(f * __uint_as_float(o[8 * k + 6]), f * __uint_as_float(o[8 * k + 7]));
+          }
+          *reinterpret_cast<uint4*>(dst + c + 8 * k) = v;
         }
-        *reinterpret_cast<uint4*>(dst + c + 8 * k) = v;
       }
+      __syncwarp();  // the next round's tcgen05.ld wants the whole warp at once
     }
   }
 

@@ -451,6 +451,7 @@ __device__ __forceinline__ void bwd_tile(const sva_diff_args& a, const sva_diff_
       load_rows<BS, D>(y2, ws.da, D_all, b, a.N, h * D, s0, a.N);
       for (int i = threadIdx.x * 4; i < kStats * 64; i += blockDim.x * 4)
         copy16(stats + st * kStats * 64 + i, ws.stats + stat_at(bh, n_stat_tiles, s0) + i);
+      __syncwarp();  // some lanes of a warp copied; its MMAs want all
     } else {
       load_rows<BS, D>(x2, a.k, a.ldk, b, Nk, h * D, s0, valid);
       load_rows<BS, D>(y2, a.v, a.ldv, b, Nk, h * D, s0, valid);

@@ -419,12 +419,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t o[32];
           tmem_ld32(o_col + c, o);
           tmem_wait_ld();
-          if (t >= a.N) continue;
-          float4* dst = reinterpret_cast<float4*>(po + r * HD + c);
+          if (t < a.N) {
+            float4* dst = reinterpret_cast<float4*>(po + r * HD + c);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+          __syncwarp();  // the next tcgen05.ld wants the whole warp at once
         }
       }
       *reinterpret_cast<float2*>(po + BQ * HD + 2 * r) = make_float2(m, l);
@@ -444,6 +446,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int64_t row = static_cast<int64_t>(b) * a.N + t;
       const float lam = row_ok ? lambda_of<__nv_bfloat16>(a, b, t, h) : 0.f;
       if (row_ok && ok) finish_lse(a, mp, b, h, t, m, l);
+      __syncwarp();  // the next tcgen05.ld wants the whole warp at once
 #pragma unroll 1
       for (int c = mp * 64; c < mp * 64 + 64 && ok; c += 32) {
         uint32_t o1[32], o2[32];
@@ -481,36 +484,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           __syncwarp();
         }
-        if (!row_ok) continue;
-        const uint8_t* grow = smem + Q_OFF + (c >> 6) * BOX + r * 128;
-        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + h * HD + c;
+        if (row_ok) {
+          const uint8_t* grow = smem + Q_OFF + (c >> 6) * BOX + r * 128;
+          __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + h * HD + c;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float x[8], y[8];
+          for (int k = 0; k < 4; ++k) {
+            float x[8], y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] = __uint_as_float(o1[8 * k + e]) * i1;
-            y[e] = __uint_as_float(o2[8 * k + e]) * i2;
+            for (int e = 0; e < 8; ++e) {
+              x[e] = __uint_as_float(o1[8 * k + e]) * i1;
+              y[e] = __uint_as_float(o2[8 * k + e]) * i2;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(-lam, y[e], x[e]);
+            if (gated) {
+              // row r of the gate tile, 128-byte swizzle: chunk i of the row at i ^ (r & 7)
+              const int chunk = ((c & 63) >> 3) + k;
+              const uint4 gv = *reinterpret_cast<const uint4*>(grow + ((chunk ^ (r & 7)) << 4));
+              const float gg[8] = {bf16lo_to_f32(gv.x), bf16hi_to_f32(gv.x), bf16lo_to_f32(gv.y),
+                                   bf16hi_to_f32(gv.y), bf16lo_to_f32(gv.z), bf16hi_to_f32(gv.z),
+                                   bf16lo_to_f32(gv.w), bf16hi_to_f32(gv.w)};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] *= __fdividef(1.0f, 1.0f + __expf(-gg[e]));
+            }
+            uint4 ov;
+            ov.x = pack_bf16x2(y[0], y[1]);
+            ov.y = pack_bf16x2(y[2], y[3]);
+            ov.z = pack_bf16x2(y[4], y[5]);
+            ov.w = pack_bf16x2(y[6], y[7]);
+            *reinterpret_cast<uint4*>(op + 8 * k) = ov;
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = fmaf(-lam, y[e], x[e]);
-          if (gated) {
-            // row r of the gate tile, 128-byte swizzle: chunk i of the row at i ^ (r & 7)
-            const int chunk = ((c & 63) >> 3) + k;
-            const uint4 gv = *reinterpret_cast<const uint4*>(grow + ((chunk ^ (r & 7)) << 4));
-            const float gg[8] = {bf16lo_to_f32(gv.x), bf16hi_to_f32(gv.x), bf16lo_to_f32(gv.y),
-                                 bf16hi_to_f32(gv.y), bf16lo_to_f32(gv.z), bf16hi_to_f32(gv.z),
-                                 bf16lo_to_f32(gv.w), bf16hi_to_f32(gv.w)};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= __fdividef(1.0f, 1.0f + __expf(-gg[e]));
-          }
-          uint4 ov;
-          ov.x = pack_bf16x2(y[0], y[1]);
-          ov.y = pack_bf16x2(y[2], y[3]);
-          ov.z = pack_bf16x2(y[4], y[5]);
-          ov.w = pack_bf16x2(y[6], y[7]);
-          *reinterpret_cast<uint4*>(op + 8 * k) = ov;
         }
+        __syncwarp();  // as above
       }
     }
   }
