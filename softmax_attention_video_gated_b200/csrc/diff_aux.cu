@@ -55,10 +55,17 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const sva_diff_args a, 
   }
 }
 
-// the gate's sigmoid: bf16 results do not see the last bits of a division
+// the gate's sigmoid s and 1 - s, which keeps its digits where s is next to 1: with e = exp(-|x|)
+// one of them is 1 / (1 + e), the other e / (1 + e). bf16 results do not see the last bits of
+// a division.
+struct Sigmoid {
+  float s, rest;
+};
 template <typename T>
-__device__ __forceinline__ float prep_sigmoid(float x) {
-  return sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + __expf(-x)) : sigmoid_f(x);
+__device__ __forceinline__ Sigmoid prep_sigmoid(float x) {
+  const float e = sizeof(T) == 2 ? __expf(-fabsf(x)) : expf(-fabsf(x));
+  const float r = sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + e) : 1.0f / (1.0f + e);
+  return x >= 0.f ? Sigmoid{r, e * r} : Sigmoid{e * r, r};
 }
 __device__ __forceinline__ float half_sum(float v) {
 #pragma unroll
@@ -107,15 +114,15 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     if (a.gate != nullptr) {
-      const float4 s = make_float4(prep_sigmoid<T>(gx[i].x), prep_sigmoid<T>(gx[i].y),
-                                   prep_sigmoid<T>(gx[i].z), prep_sigmoid<T>(gx[i].w));
-      const float4 y = make_float4(d[i].x * s.x, d[i].y * s.y, d[i].z * s.z, d[i].w * s.w);
+      const Sigmoid sx = prep_sigmoid<T>(gx[i].x), sy = prep_sigmoid<T>(gx[i].y),
+                    sz = prep_sigmoid<T>(gx[i].z), sw = prep_sigmoid<T>(gx[i].w);
+      const float4 y = make_float4(d[i].x * sx.s, d[i].y * sy.s, d[i].z * sz.s, d[i].w * sw.s);
       if (in)
         store4(static_cast<T*>(g.dgate) + row * g.lddg + col + 64 * i,
-               make_float4(y.x * fmaf(-lam, o2[i].x, o1[i].x) * (1.f - s.x),
-                           y.y * fmaf(-lam, o2[i].y, o1[i].y) * (1.f - s.y),
-                           y.z * fmaf(-lam, o2[i].z, o1[i].z) * (1.f - s.z),
-                           y.w * fmaf(-lam, o2[i].w, o1[i].w) * (1.f - s.w)));
+               make_float4(y.x * fmaf(-lam, o2[i].x, o1[i].x) * sx.rest,
+                           y.y * fmaf(-lam, o2[i].y, o1[i].y) * sy.rest,
+                           y.z * fmaf(-lam, o2[i].z, o1[i].z) * sz.rest,
+                           y.w * fmaf(-lam, o2[i].w, o1[i].w) * sw.rest));
       d[i] = y;
     }
     dl -= dot4(d[i], o2[i]);

@@ -63,19 +63,24 @@ __device__ __forceinline__ int key_count(const int32_t* key_lens, int b, int Nk)
   return key_lens == nullptr ? Nk : max(0, min(Nk, key_lens[b]));
 }
 
-// lambda of token t (batch b, head h)
+// lam of token t (batch b, head h), and the lambda that it stands for
+template <typename T>
+__device__ __forceinline__ float lambda_arg(const sva_diff_args& a, int b, int64_t t, int h) {
+  const T* p = static_cast<const T*>(a.lam);
+  return to_f32(a.ldl == 0 ? p[h] : p[(static_cast<int64_t>(b) * a.N + t) * a.ldl + h]);
+}
 template <typename T>
 __device__ __forceinline__ float lambda_of(const sva_diff_args& a, int b, int64_t t, int h) {
-  const T* p = static_cast<const T*>(a.lam);
-  const float x = to_f32(a.ldl == 0 ? p[h] : p[(static_cast<int64_t>(b) * a.N + t) * a.ldl + h]);
+  const float x = lambda_arg<T>(a, b, t, h);
   return (a.flags & SVA_FLAG_LAMBDA_VALUE) ? x : sigmoid_f(x);
 }
 
 // What dlambda's sum is multiplied by in the end, 1 for lambda as a value: the sum for a
-// sigmoid's lambda carries the factor lambda already (dsigma = lambda (1 - lambda)).
+// sigmoid's lambda carries the factor lambda already (dsigma = lambda (1 - lambda)), and
+// 1 - sigma(x) is sigma(-x), which keeps its digits where lambda is next to 1.
 template <typename T>
 __device__ __forceinline__ float dlambda_factor(const sva_diff_args& a, int b, int64_t t, int h) {
-  return (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : 1.f - lambda_of<T>(a, b, t, h);
+  return (a.flags & SVA_FLAG_LAMBDA_VALUE) ? 1.f : sigmoid_f(-lambda_arg<T>(a, b, t, h));
 }
 
 // 1 / l of a row's sum. Without a key l is zero, and so is the row; with keys it is 2^-8 at

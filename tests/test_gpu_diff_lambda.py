@@ -70,8 +70,8 @@ def exact(t, H, flags):
     if t["lam"].ndim == 1:
         ref, terms = ref.sum((0, 1)), terms.sum((0, 1))
     if not flags:
-        s = torch.sigmoid(t["lam"].double())
-        ref, terms = ref * s * (1 - s), terms * (s * (1 - s)).square()
+        s = torch.sigmoid(t["lam"].double()) * torch.sigmoid(-t["lam"].double())
+        ref, terms = ref * s, terms * s.square()
     return ref, terms.sqrt()
 
 
@@ -124,3 +124,38 @@ def test_shared_lambda_of_zero_as_a_value():
     t["lam"][1] = -0.0
     assert_within(t, 2, "bf16", VALUE)
     assert math.isfinite(float(dlam_of(t, 2, VALUE).sum()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("logit", [9.0, 15.0, -15.0, 40.0, -40.0])
+@pytest.mark.parametrize("N", [2, 130])
+def test_gates_and_lambdas_far_from_zero(dtype, shared, logit, N):
+    # s (1 - s) keeps its digits where the sigmoid s is next to 1: the library's bounds, of gradients
+    # that are all of one size
+    H = 2
+    t = inputs(1, N, 150, H, dtype, 17, shared)
+    t["g"].fill_(logit)
+    t["lam"].fill_(logit)
+    for flags in (0, VALUE):
+        lam = t["lam"] if not flags else torch.full_like(t["lam"], 0.8)
+        assert_within({**t, "lam": lam}, H, dtype, flags)
+    saved = tuple(torch.empty(1, N, H * 128, device="cuda") for _ in range(2)) + \
+        (torch.empty(2, 1, H, N, device="cuda"),)
+    sva.sva_diff_anchor_fwd(t["q"], t["k"], t["v"], t["g"], t["lam"], torch.empty_like(t["q"]), H, saved=saved)
+    g = [torch.empty_like(t[n]) for n in ("q", "k", "v", "g", "lam")]
+    sva.sva_diff_anchor_bwd(t["q"], t["k"], t["v"], t["g"], t["lam"], t["dout"], saved, *g, H)
+    s, s1 = (torch.sigmoid(torch.tensor(x, dtype=torch.float64)) for x in (logit, -logit))
+    ref = torch.empty(1, N, H, 128, device="cuda", dtype=torch.float64)
+    for h in range(H):
+        c = slice(h * 128, (h + 1) * 128)
+        o = []
+        for m in (0, 64):
+            i = slice(h * 128 + m, h * 128 + m + 64)
+            o.append(torch.softmax(t["q"][0, :, i].double() @ t["k"][0, :, i].double().T / 8, 1) @
+                     t["v"][0, :, c].double())
+        lam = (t["lam"][h] if shared else t["lam"][0, :, h, None]).double()
+        ref[0, :, h] = t["dout"][0, :, c].double() * (o[0] - torch.sigmoid(lam) * o[1]) * (s * s1).item()
+    ref = ref.reshape(1, N, -1)
+    rel = float((g[3].double() - ref).norm() / ref.norm())
+    assert rel <= (1e-2 if dtype == "bf16" else 1e-5), rel
