@@ -187,11 +187,26 @@ sva_status_t sva_softmax_anchor_fwd(const sva_attn_args* args, void* ws, size_t 
  * Supported: SVA_BF16 with d = 128 (tcgen05 kernels), SVA_F32 with d in
  * {64, 128}. Any N >= 1 and n_keys >= 1 with B*max(N, n_keys) and B*H*N below
  * 2^31 and B*H at most 65,535.
+ * The published form of differential attention (Ye et al., Differential
+ * Transformer, 2024) also normalises every head behind the subtraction and scales
+ * it by 1 - lambda_init. Here the anchor's gate stands in that place; such a norm
+ * is not part of the call.
+ *
+ * Precision: products, sums and exponentials are fp32. From five queries on, SVA_BF16
+ * rounds each map's weights to bf16 for the product with V, as sva_softmax_anchor_fwd
+ * does, so that out and dG are off by about 2e-3 (2^-8 at most) of |O_1| and
+ * |lambda O_2|, O_m = P_m V, and not of their difference: where the maps nearly
+ * cancel, more than that of the result. All other gradients are made of weights
+ * recomputed in fp32, and rounded to bf16 in products alone. SVA_F32 splits its
+ * operands in 22 bits and is as exact as fp32 arithmetic. dlambda, summed over
+ * tokens where lam is shared, is off by its own rounding and 2^-14 (fp32: 1e-5) of
+ * its terms dA_c O_2c taken together.
  *
  * Training: give o1, o2 (fp32 [B, N, D], contiguous: the two maps' outputs
  * P_m V; in 32 bits, since dG and dlambda are made of them) and lse (fp32
- * [2][B][H][N]: log-sum-exp of each map's scaled logits, -infinity where a batch has no key) to the forward call, all three or none,
- * and the same to sva_diff_anchor_bwd, which computes from dout ([B, N, >=D])
+ * [2][B][H][N]: log-sum-exp of each map's scaled logits, -infinity where a batch has
+ * no key) to the forward call, all three or none, and the same to
+ * sva_diff_anchor_bwd, which computes from dout ([B, N, >=D])
  *     dA = dout * sigmoid(G),  dG = dout * A * sigmoid'(G)
  *     delta_m[t] = dA_t . O_m[t],  dlambda_t = -delta_2[t]
  *     dV = (P_1 - lambda P_2)^T dA,   dP = dA V^T
@@ -202,7 +217,7 @@ sva_status_t sva_softmax_anchor_fwd(const sva_attn_args* args, void* ws, size_t 
  * all tokens, [H]; each in dtype. dgate must be NULL exactly when gate is. All
  * gradients are written whole (not added to), dk and dv with zeros at and
  * behind key_lens[b]. A padded batch's own padding among the queries takes part
- * unless its dout rows are zero (and its q rows finite). Gradients may not
+ * unless its dout rows are zero (and its q, gate and lam finite). Gradients may not
  * overlap the inputs. No atomics: the same call gives the same bits.
  */
 typedef struct {
