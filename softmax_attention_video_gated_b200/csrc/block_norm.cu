@@ -23,8 +23,10 @@
 // (g_b w_post, w_pre (1 + s_b), t_b). The column sums stay in registers over a
 // CTA's rows, leave once per CTA, and are summed by a second kernel in a fixed
 // order.
-// 16,380 rows of 2,048 channels in bf16 (402 MB forward, 604 MB backward): 78 us a call
-// forward, 5.1 TB/s, 0.79 of the measured copy rate; backward 97 us and 10 for the sums.
+// 16,380 rows of 2,048 channels in bf16 (402 MB forward, 604 MB backward): 75 us a call
+// forward, 5.4 TB/s, 0.82 of the measured copy rate; forward and backward 188, the backward
+// kernel 94 alone and 10 for the sums. Above 6,144 channels a backward row leaves room for
+// one stage, and its loads are waited for: 8,192 channels 3.7 TB/s where 6,144 reach 5.5.
 // The backward pass keeps 48 sums and a row a thread in registers: at 128 of them it
 // spilled, and next to this much shared memory L1 holds no spills (180 us).
 #include <algorithm>

@@ -35,7 +35,7 @@
 // cancels. It is one addition per pair and map 2, on dS_2 before its rounding, and takes 35
 // us of a training step of 8,190 tokens and 16 heads (3.40 -> 3.44 ms).
 //
-// 8,190 tokens of 16 heads: 2.2 to 2.4 ms for both sides, 570 to 620 TFLOP/s of
+// 8,190 tokens of 16 heads: 2.4 to 2.5 ms for both sides, 550 to 570 TFLOP/s of
 // the 10 d operations a pair that the gradients need; the steps there: MMAs behind elect.sync in uniform code
 // 3.2 -> 2.8 ms, two warps of weights a scheduler -> four without a spilled register
 // (16 columns a thread, dP's registers free before S's are read) 2.86 -> 2.26 ms. A
@@ -46,7 +46,7 @@
 // would take 0.35 ms less, without the exponentials as much less. Queries standing: the
 // weights' instructions (0.93 ms of it). Sending exponentials to the FMA pipe costs here.
 // Few long tiles are cut along their stream over the CTAs of a cluster, which add up in
-// the order of the cuts: 64 queries against 4,000 keys, 8 heads, 89 -> 60 us.
+// the order of the cuts: 64 queries against 4,000 keys, 8 heads, 89 -> 60 us call after call.
 #include <algorithm>
 
 #include "diff_common.cuh"

@@ -17,12 +17,15 @@
 // is off by half a step, 2^-8 of the weight, at most and at random: the result is off by
 // 0.0026 (relative L2) where its own rounding alone is 0.0017. P in more bits would double
 // its product.
-// What bounds it: the exponentials, two per pair of a query and a key and product with
-// V. 8,190 tokens of 16 heads (1,024 CTAs) take 770 us, 1,070 TFLOP/s, 0.65 of the
-// measured bf16 peak; without exponentials it would take 595 us, with half of them 651.
-// A quarter of them therefore runs on the FMA pipe (823 -> 772 us). Tried and slower:
-// two warpgroups a map with half of the keys each (862), P reported in halves (795),
-// the maximum begun on half of S (879).
+// Where the maps nearly cancel that is 0.002 of each map's output, not of the difference.
+// What bounds it: the chain of one map, S -> softmax -> P -> P V, whose S has one buffer
+// that P lies over; tensor pipe and MUFU are both busy half of the time. 8,190 tokens of
+// 16 heads (1,024 CTAs) take 870 to 890 us call after call, 940 TFLOP/s, 0.57 of the
+// measured bf16 peak (850 alone, behind a pause). The softmax is the longer half of the
+// chain: on a box and clock where it took 823 us, it took 595 without exponentials and 651
+// with half of them, so a quarter runs on the FMA pipe (823 -> 772 there). Tried and slower
+// than those 772: two warpgroups a map with half of the keys each (862), P reported in
+// halves (795), the maximum begun on half of S (879).
 // At the end both warpgroups read both maps' O (a TMEM lane quarter belongs to a
 // warp's place in its warpgroup, so the two share it), half of the columns each,
 // and combine them with lambda, the sums and the gate.

@@ -162,7 +162,15 @@ struct DiffPlan {
   size_t partial_bytes = 0;
   unsigned grid() const { return static_cast<unsigned>(n_full + n_split_units * split); }
 };
-// at most this many queries a batch go to the kernel that reads K and V once
+// At most this many queries a batch go to the kernel that reads K and V once. 16 heads, B = 1, us
+// forward/gradients, that kernel and a tile of queries with the merge of its parts (bf16; the
+// tile's do not depend on N):
+//     keys    N = 1    2        3, 4      tile
+//     300     12/14    14/16    18/27     20/18
+//     2,000   16/23    23/27    41/47     27/49
+//     8,190   31/49    45/63    88/125    39/119
+// fp32: 43/80, 59/106, 80/131 against 160/534 at 8,190 keys. Three and four rows in bf16 are
+// slower forward behind 2,000 keys; they stay here for their unrounded weights.
 constexpr int kDiffFewRows = 4;
 // (it waits for nothing, reports nothing and writes the status words itself)
 cudaError_t diff_fwd_few(const sva_diff_args& a, int* status, cudaStream_t s);
